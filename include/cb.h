@@ -15,6 +15,10 @@
  *   4. cb_step_done      (host)  commits the step: advances each request,
  *      finishes requests and returns their blocks to the pool.
  *
+ * An 8-bit cache takes the place of steps 2 and 3 by cb_kv_append_q8 (which
+ * can also rotate q and k, cb_rope) and cb_paged_attention_q8; the tables of
+ * step 1 can also be kept and built on the GPU (cb_step_tables).
+ *
  * Around the step: cb_kv_swap (GPU) moves offloaded requests' blocks to and
  * from a pinned host swap pool; cb_validate_step (host) checks a step's
  * metadata; cb_paged_decode_noalloc runs decode rows without a caller
@@ -459,6 +463,10 @@ typedef struct cb_attention_args {
                                        row's queries outside [0, num_tokens) */
 #define CB_DEVERR_TIMEOUT 0x10u     /* a bounded wait ran out */
 #define CB_DEVERR_PLAN 0x20u        /* decode splits did not fit the partial slots */
+#define CB_DEVERR_NO_BLOCKS 0x40u   /* the ring of free blocks ran out, or was
+                                       given back more than it holds */
+#define CB_DEVERR_SLOT_ORDER 0x80u  /* neighbouring tokens of one block whose
+                                       slots do not follow each other */
 
 /* Workspace bytes for calls with up to num_reqs rows and these head sizes
  * (0 on bad args).  One workspace serves any later call with at most that
@@ -478,6 +486,215 @@ cb_status cb_paged_attention(const cb_attention_args* args, cb_stream_t stream);
  * workspace.  Returns CB_ERR_DEVICE_CHECK if any bit was set. */
 cb_status cb_attention_read_errors(void* workspace, size_t workspace_bytes,
                                    cb_stream_t stream, uint32_t* bits);
+
+/* ------------------------------------------------------------------------
+ * Tables built on the GPU.  "vLLM serving internals", PagedAttention as a
+ * virtual memory system: a sequence's block table maps its positions to
+ * blocks, blocks come from a free list and go back to it.  Here the tables,
+ * the free list and the lengths stay in device memory: a step is given only
+ * its rows' query lengths, so it can be captured in a CUDA graph and run
+ * without the host's scheduler between steps.
+ *
+ * State, in place: cached_lens [num_rows], block_tables [num_rows]
+ * [max_blocks_per_seq], and the free blocks as a ring of num_blocks ids:
+ * free_state[0] = head (in [0, num_blocks)), free_state[1] = count; entry
+ * (head + i) % num_blocks for i in [0, count) is free.
+ *
+ * cb_step_tables appends q_lens[r] tokens to every row r (0: none).  In row
+ * order, each row takes ceil((cached + q) / block_size) - ceil(cached /
+ * block_size) blocks from the ring's head into its next table entries, then
+ * cached_lens[r] += q.  It writes
+ *   cu_seqlens_q [num_rows + 1]  prefix sums of the query lengths
+ *   seq_lens [num_rows]          cached + q; 0 for a row without queries
+ *                                (the padding row of cb_paged_attention)
+ *   slot_mapping [max_tokens]    each token's slot; -1 past the last token
+ *   positions [max_tokens]       each token's position; 0 past the last
+ * A row that cannot be served is dropped: it gets no queries (seq_lens 0),
+ * its state stays, and a bit is set in error_word (optional).  Dropped are
+ * rows with a negative length or more than max_blocks_per_seq blocks
+ * (CB_DEVERR_SEQ_RANGE); of the others, from the first whose tokens pass
+ * max_tokens on, every row with queries (CB_DEVERR_SEQ_RANGE); of the
+ * others, from the first whose blocks pass the free ones on, every row that
+ * needs a block (CB_DEVERR_NO_BLOCKS).  A table or ring entry outside
+ * [0, num_blocks) gives its tokens slot -1 and sets CB_DEVERR_BLOCK_RANGE.
+ *
+ * cb_trim_tables shortens rows to keep_lens[r] tokens (negative, or equal to
+ * cached_lens[r]: the row stays; 0: its request ended): the blocks past
+ * ceil(keep / block_size) go to the ring's tail, in row order then table
+ * order, their table entries become -1, cached_lens[r] = keep.  A row with
+ * keep_lens[r] > cached_lens[r], or with more blocks than its table, stays
+ * (CB_DEVERR_SEQ_RANGE); from the first row whose blocks would overfill the
+ * ring on, every row that gives blocks stays (CB_DEVERR_NO_BLOCKS).  An id
+ * outside the pool is passed on as it is (CB_DEVERR_BLOCK_RANGE).
+ *
+ * block_size is a power of two; at most CB_TABLES_MAX_ROWS rows and 2^31 /
+ * block_size blocks (CB_ERR_UNSUPPORTED otherwise).  The arrays do not
+ * overlap; calls that share state run one after the other.
+ * ---------------------------------------------------------------------- */
+#define CB_TABLES_MAX_ROWS 8192
+typedef struct cb_tables {
+  int32_t num_rows;
+  int32_t max_blocks_per_seq;
+  int32_t num_blocks;           /* pool size, and entries of free_ring */
+  int32_t block_size;
+  int32_t* cached_lens;         /* device [num_rows], in and out */
+  int32_t* block_tables;        /* device [num_rows][max_blocks_per_seq], in and out */
+  int32_t* free_ring;           /* device [num_blocks], in and out */
+  int32_t* free_state;          /* device [2]: head, count, in and out */
+  uint32_t* error_word;         /* optional device word */
+} cb_tables;
+
+cb_status cb_step_tables(const cb_tables* tables, const int32_t* q_lens, int32_t max_tokens,
+                         int32_t* cu_seqlens_q, int32_t* seq_lens, int32_t* slot_mapping,
+                         int32_t* positions, cb_stream_t stream);
+
+cb_status cb_trim_tables(const cb_tables* tables, const int32_t* keep_lens, cb_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Rotary positions.  The first rot_dim dims of a head form pairs (a_i, b_i),
+ * i in [0, rot_dim / 2): dims (i, i + rot_dim / 2) in the half layout,
+ * (2i, 2i + 1) in the interleaved one.  At position p a pair becomes
+ *   (a c - b s, b c + a s),  c = m cos(p f_i), s = m sin(p f_i);
+ * with `inverse`, s is negated: the transpose of that product, so it turns
+ * gradients of the outputs into gradients of the inputs.  The other dims are
+ * copied.  Arithmetic is float32, rounded once.
+ *
+ * A plan holds the frequencies as 64-bit fractions of a turn per position,
+ * turns[i] = f_i / (2 pi) * 2^64, so that p * turns[i] modulo 2^64 is the
+ * angle at any position (of either sign) without loss.  cb_rope_plan_init
+ * fills one on the host; a caller with frequencies of its own fills
+ * the struct itself.  With f_i = base^(-2i / rot_dim):
+ *   CB_ROPE_LINEAR  f_i / factor
+ *   CB_ROPE_NTK     f_i of the base base * factor^(rot_dim / (rot_dim - 2))
+ *   CB_ROPE_PARTS   f_i (k_i + (1 - k_i) / factor), k_i = 1 - clamp((i - lo)
+ *                   / (hi - lo), 0, 1), lo = floor(at(beta_fast)) >= 0, hi =
+ *                   ceil(at(beta_slow)) <= rot_dim / 2 - 1 (lo + 0.001 if
+ *                   they are equal), at(n) = rot_dim ln(original_positions /
+ *                   (2 pi n)) / (2 ln base); m = 0.1 ln(factor) + 1
+ *   CB_ROPE_BANDS   the same with k_i = clamp((n_i - low_freq_factor) /
+ *                   (high_freq_factor - low_freq_factor), 0, 1), n_i =
+ *                   original_positions f_i / (2 pi); m = 1
+ * ---------------------------------------------------------------------- */
+#define CB_ROPE_MAX_PAIRS 128
+#define CB_ROPE_HALF 0
+#define CB_ROPE_INTERLEAVED 1
+#define CB_ROPE_NONE 0
+#define CB_ROPE_LINEAR 1
+#define CB_ROPE_NTK 2
+#define CB_ROPE_PARTS 3
+#define CB_ROPE_BANDS 4
+
+typedef struct cb_rope_config {
+  int32_t head_dim;
+  int32_t rot_dim;              /* even, 2 .. min(head_dim, 2 * CB_ROPE_MAX_PAIRS) */
+  int32_t layout;               /* CB_ROPE_HALF, CB_ROPE_INTERLEAVED */
+  int32_t scaling;              /* CB_ROPE_NONE .. CB_ROPE_BANDS */
+  double base;                  /* > 1 */
+  double factor;                /* >= 1 (scalings other than NONE) */
+  double original_positions;    /* >= 1 (PARTS, BANDS) */
+  double beta_fast, beta_slow;  /* beta_fast > beta_slow > 0 (PARTS) */
+  double low_freq_factor, high_freq_factor; /* high > low > 0 (BANDS) */
+  double amplitude;             /* m; 0: the scaling's own */
+} cb_rope_config;
+
+typedef struct cb_rope_plan {
+  int32_t head_dim;
+  int32_t rot_dim;
+  int32_t layout;
+  float amplitude;
+  uint64_t turns[CB_ROPE_MAX_PAIRS];
+} cb_rope_plan;
+
+cb_status cb_rope_plan_init(const cb_rope_config* config, cb_rope_plan* plan);
+
+/* Rotates the rows q [num_tokens][num_q_heads][head_dim] and k [num_tokens]
+ * [num_kv_heads][head_dim] by positions[t].  Either of q and k may be NULL.
+ * The strides are elements from a token to the next (0: packed, heads *
+ * head_dim), so q and k may lie in one [tokens][all heads] array.  An output
+ * may be its input with the same stride; other overlaps are undefined.
+ * Pointers are aligned to their element. */
+typedef struct cb_rope_args {
+  const cb_rope_plan* plan;     /* host */
+  const int32_t* positions;     /* device [num_tokens] */
+  int32_t num_tokens;
+  int32_t num_q_heads;
+  int32_t num_kv_heads;
+  cb_dtype dtype;
+  int32_t inverse;
+  const void* q;
+  void* q_out;
+  int64_t q_stride, q_out_stride;
+  const void* k;
+  void* k_out;
+  int64_t k_stride, k_out_stride;
+} cb_rope_args;
+
+cb_status cb_rope(const cb_rope_args* args, cb_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * The 8-bit cache.  k_cache and v_cache hold e4m3 codes in the layout of the
+ * 16-bit caches, [num_blocks][Hkv][16][D] bytes; k_scales and v_scales hold
+ * one byte s for each (block, KV head), scale_stride bytes from a block's
+ * first to the next block's.  An element's value is code * 2^(s - 127).
+ * Scales are powers of two: e4m3 keeps its four bits at every exponent, so a
+ * finer scale would not make the codes better, and with these a code times
+ * its scale is a bfloat16 number exactly and codes can move to a larger
+ * scale with no second rounding of a normal one.  s - 127 lies in [-40, 40]; the attention reads
+ * a byte outside that as the nearest inside.
+ *
+ * cb_kv_append_q8 writes a step's new K/V.  For each block and KV head that
+ * the call's tokens touch, e = the least integer with |x| <= 448 * 2^e for
+ * every finite new x there (in [-40, 40]).  A block whose offset 0 is
+ * written starts afresh with that e; another keeps its old exponent if that
+ * is larger, and otherwise the codes at the offsets before the first new one
+ * are requantised to the new one.  Codes are x * 2^-e rounded to nearest
+ * even; finite values past 448 * 2^40 become 448 * 2^40, an infinity becomes
+ * NaN.  Offsets after the new tokens are not touched.
+ *   - slot_mapping: -1 = padding, skipped.  The tokens of one block are one
+ *     run: neighbours in the call, at increasing neighbouring offsets, as
+ *     the scheduler and cb_step_tables emit them.  Of two neighbouring
+ *     tokens in one block that break the order the later one's run is skipped
+ *     (CB_DEVERR_SLOT_ORDER); with runs of one block that are not
+ *     neighbours the block's contents are undefined (CB_VALIDATE=1 finds
+ *     those).  A slot outside the pool is skipped (CB_DEVERR_SLOT_RANGE).
+ *   - rope (optional): k is rotated in float32 before it is quantised, and
+ *     q [num_tokens][Hq][D] (optional) is rotated into q_out.  rot_dim is
+ *     then a multiple of 16.
+ * D is 64 or 128, block_size 16; all pointers but the scales' 16-byte
+ * aligned.
+ * ---------------------------------------------------------------------- */
+typedef struct cb_append_q8_args {
+  const void* k_new;            /* device [num_tokens][Hkv][D] (dtype) */
+  const void* v_new;
+  const int32_t* slot_mapping;  /* device [num_tokens] */
+  int32_t num_tokens;
+  cb_dtype dtype;
+  void* k_cache;                /* device [num_blocks][Hkv][16][D] e4m3 */
+  void* v_cache;
+  uint8_t* k_scales;            /* device [num_blocks][scale_stride] */
+  uint8_t* v_scales;
+  int64_t scale_stride;         /* >= Hkv; 0: Hkv */
+  int32_t num_blocks;
+  int32_t num_kv_heads;
+  int32_t head_dim;
+  int32_t block_size;
+  const cb_rope_plan* rope;     /* optional, host */
+  const int32_t* positions;     /* device [num_tokens], with rope */
+  const void* q;                /* optional, with rope */
+  void* q_out;                  /* may be q */
+  int32_t num_q_heads;
+  uint32_t* error_word;         /* optional device word */
+} cb_append_q8_args;
+
+cb_status cb_kv_append_q8(const cb_append_q8_args* args, cb_stream_t stream);
+
+/* cb_paged_attention over an 8-bit cache: the same rows, masks, workspace,
+ * padding and error bits; q and out are of args->dtype, args->k_cache and
+ * v_cache hold codes.  Any number of query heads per KV head.  after_append
+ * refers to this step's cb_kv_append_q8. */
+cb_status cb_paged_attention_q8(const cb_attention_args* args, const uint8_t* k_scales,
+                                const uint8_t* v_scales, int64_t scale_stride,
+                                cb_stream_t stream);
 
 /* ------------------------------------------------------------------------
  * cb_debug_inject_wait_timeout (test hook; no counterpart in the pages).

@@ -38,6 +38,8 @@ DEVERR_DECODE_QLEN = 0x4
 DEVERR_SEQ_RANGE = 0x8
 DEVERR_TIMEOUT = 0x10
 DEVERR_PLAN = 0x20
+DEVERR_NO_BLOCKS = 0x40
+DEVERR_SLOT_ORDER = 0x80
 
 
 class CBError(RuntimeError):
@@ -124,6 +126,55 @@ class cb_swap_args(ctypes.Structure):
                 ("block_bytes", ctypes.c_int64), ("error_word", ctypes.c_void_p)]
 
 
+class cb_tables(ctypes.Structure):
+    _fields_ = [("num_rows", ctypes.c_int32), ("max_blocks_per_seq", ctypes.c_int32),
+                ("num_blocks", ctypes.c_int32), ("block_size", ctypes.c_int32),
+                ("cached_lens", ctypes.c_void_p), ("block_tables", ctypes.c_void_p),
+                ("free_ring", ctypes.c_void_p), ("free_state", ctypes.c_void_p),
+                ("error_word", ctypes.c_void_p)]
+
+
+ROPE_MAX_PAIRS = 128
+
+
+class cb_rope_config(ctypes.Structure):
+    _fields_ = [("head_dim", ctypes.c_int32), ("rot_dim", ctypes.c_int32),
+                ("layout", ctypes.c_int32), ("scaling", ctypes.c_int32),
+                ("base", ctypes.c_double), ("factor", ctypes.c_double),
+                ("original_positions", ctypes.c_double), ("beta_fast", ctypes.c_double),
+                ("beta_slow", ctypes.c_double), ("low_freq_factor", ctypes.c_double),
+                ("high_freq_factor", ctypes.c_double), ("amplitude", ctypes.c_double)]
+
+
+class cb_rope_plan(ctypes.Structure):
+    _fields_ = [("head_dim", ctypes.c_int32), ("rot_dim", ctypes.c_int32),
+                ("layout", ctypes.c_int32), ("amplitude", ctypes.c_float),
+                ("turns", ctypes.c_uint64 * ROPE_MAX_PAIRS)]
+
+
+class cb_rope_args(ctypes.Structure):
+    _fields_ = [("plan", ctypes.POINTER(cb_rope_plan)), ("positions", ctypes.c_void_p),
+                ("num_tokens", ctypes.c_int32), ("num_q_heads", ctypes.c_int32),
+                ("num_kv_heads", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("inverse", ctypes.c_int32), ("q", ctypes.c_void_p), ("q_out", ctypes.c_void_p),
+                ("q_stride", ctypes.c_int64), ("q_out_stride", ctypes.c_int64),
+                ("k", ctypes.c_void_p), ("k_out", ctypes.c_void_p),
+                ("k_stride", ctypes.c_int64), ("k_out_stride", ctypes.c_int64)]
+
+
+class cb_append_q8_args(ctypes.Structure):
+    _fields_ = [("k_new", ctypes.c_void_p), ("v_new", ctypes.c_void_p),
+                ("slot_mapping", ctypes.c_void_p), ("num_tokens", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("k_cache", ctypes.c_void_p),
+                ("v_cache", ctypes.c_void_p), ("k_scales", ctypes.c_void_p),
+                ("v_scales", ctypes.c_void_p), ("scale_stride", ctypes.c_int64),
+                ("num_blocks", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("block_size", ctypes.c_int32),
+                ("rope", ctypes.POINTER(cb_rope_plan)), ("positions", ctypes.c_void_p),
+                ("q", ctypes.c_void_p), ("q_out", ctypes.c_void_p),
+                ("num_q_heads", ctypes.c_int32), ("error_word", ctypes.c_void_p)]
+
+
 def _declare():
     L = _lib
     P = ctypes.POINTER
@@ -154,6 +205,12 @@ def _declare():
     L.cb_paged_attention.argtypes = [P(cb_attention_args), vp]
     L.cb_attention_read_errors.argtypes = [vp, sz, vp, P(ctypes.c_uint32)]
     L.cb_debug_inject_wait_timeout.argtypes = [ctypes.c_uint64, i32, i32]
+    L.cb_step_tables.argtypes = [P(cb_tables), vp, i32, vp, vp, vp, vp, vp]
+    L.cb_trim_tables.argtypes = [P(cb_tables), vp, vp]
+    L.cb_rope_plan_init.argtypes = [P(cb_rope_config), P(cb_rope_plan)]
+    L.cb_rope.argtypes = [P(cb_rope_args), vp]
+    L.cb_kv_append_q8.argtypes = [P(cb_append_q8_args), vp]
+    L.cb_paged_attention_q8.argtypes = [P(cb_attention_args), vp, vp, i64, vp]
     PV = P(vp)
     L.cb_executor_create.argtypes = [P(cb_executor_config), P(vp)]
     L.cb_executor_destroy.argtypes = [vp]
@@ -174,7 +231,9 @@ def _declare():
                  "cb_paged_attention", "cb_attention_read_errors",
                  "cb_debug_inject_wait_timeout", "cb_executor_create", "cb_executor_submit",
                  "cb_executor_run_step", "cb_executor_synchronize", "cb_executor_stats",
-                 "cb_executor_reset_stats", "cb_executor_read_errors"):
+                 "cb_executor_reset_stats", "cb_executor_read_errors", "cb_step_tables",
+                 "cb_trim_tables", "cb_rope_plan_init", "cb_rope", "cb_kv_append_q8",
+                 "cb_paged_attention_q8"):
         getattr(L, name).restype = ctypes.c_int
 
 
@@ -503,6 +562,239 @@ def paged_attention(q, k_cache, v_cache, cu_seqlens_q, seq_lens, block_tables, *
     return out
 
 
+# ------------------------------------------- the 8-bit cache and its operators
+def _need_i32(name, t, shape):
+    torch = _torch()
+    _need_cuda(t)
+    if t.dtype != torch.int32 or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be int32 of shape {tuple(shape)}")
+
+
+def _need_one_device(first, *ts):
+    """Every tensor on the first one's device, and that one current: the
+    launch goes to the current device's stream."""
+    for t in ts:
+        if t is not None and t.device != first.device:
+            raise ValueError("tensors live on different devices")
+    if first.device.index != _torch().cuda.current_device():
+        raise ValueError("the tensors' device is not the current device")
+
+
+def _tables(cached_lens, block_tables, free_ring, free_state, block_size, error_word):
+    R = cached_lens.shape[0]
+    _need_i32("cached_lens", cached_lens, (R,))
+    _need_i32("block_tables", block_tables, (R, block_tables.shape[-1]))
+    _need_i32("free_ring", free_ring, (free_ring.shape[0],))
+    _need_i32("free_state", free_state, (2,))
+    _need_one_device(cached_lens, block_tables, free_ring, free_state, error_word)
+    return cb_tables(R, block_tables.shape[1], free_ring.shape[0], int(block_size),
+                     cached_lens.data_ptr(), block_tables.data_ptr(), free_ring.data_ptr(),
+                     free_state.data_ptr(),
+                     error_word.data_ptr() if error_word is not None else None)
+
+
+def step_tables(q_lens, cached_lens, block_tables, free_ring, free_state, *, cu_seqlens_q,
+                seq_lens, slot_mapping, positions, block_size: int = 16, error_word=None,
+                stream=None) -> None:
+    """cb_step_tables: append ``q_lens`` [R] tokens to the rows of a device
+    state (``cached_lens`` [R], ``block_tables`` [R, W], the ring of free
+    blocks ``free_ring`` [num_blocks] with ``free_state`` = [head, count]; all
+    int32, updated in place) and write the step's ``cu_seqlens_q`` [R + 1],
+    ``seq_lens`` [R], ``slot_mapping`` [T] and ``positions`` [T]."""
+    t = _tables(cached_lens, block_tables, free_ring, free_state, block_size, error_word)
+    R, T = t.num_rows, slot_mapping.shape[0]
+    for name, x, n in (("q_lens", q_lens, R), ("cu_seqlens_q", cu_seqlens_q, R + 1),
+                       ("seq_lens", seq_lens, R), ("slot_mapping", slot_mapping, T),
+                       ("positions", positions, T)):
+        _need_i32(name, x, (n,))
+    _need_one_device(cached_lens, q_lens, cu_seqlens_q, seq_lens, slot_mapping, positions)
+    _check(_lib.cb_step_tables(ctypes.byref(t), q_lens.data_ptr(), T, cu_seqlens_q.data_ptr(),
+                               seq_lens.data_ptr(), slot_mapping.data_ptr(),
+                               positions.data_ptr(), _stream_ptr(stream)))
+
+
+def trim_tables(keep_lens, cached_lens, block_tables, free_ring, free_state, *,
+                block_size: int = 16, error_word=None, stream=None) -> None:
+    """cb_trim_tables: shorten the rows of a device state to ``keep_lens`` [R]
+    tokens (negative: the row stays; 0: its request ended) and give their
+    blocks back to the ring."""
+    t = _tables(cached_lens, block_tables, free_ring, free_state, block_size, error_word)
+    _need_i32("keep_lens", keep_lens, (t.num_rows,))
+    _need_one_device(cached_lens, keep_lens)
+    _check(_lib.cb_trim_tables(ctypes.byref(t), keep_lens.data_ptr(), _stream_ptr(stream)))
+
+
+ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
+ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "parts": 3, "bands": 4}
+
+
+class RopePlan:
+    """cb_rope_plan: the rotary frequencies of heads of ``head_dim`` dims
+    whose first ``rot_dim`` (default: all) rotate.  ``layout`` "half" pairs
+    dims (i, i + rot_dim / 2), "interleaved" pairs (2i, 2i + 1); ``scaling``
+    "none", "linear", "ntk", "parts" or "bands" (include/cb.h has the
+    formulas).  Host data; it is copied at each call."""
+
+    def __init__(self, head_dim: int, rot_dim: Optional[int] = None, *, layout: str = "half",
+                 base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+                 original_positions: float = 0.0, beta_fast: float = 32.0, beta_slow: float = 1.0,
+                 low_freq_factor: float = 1.0, high_freq_factor: float = 4.0,
+                 amplitude: float = 0.0):
+        if layout not in ROPE_LAYOUTS or scaling not in ROPE_SCALINGS:
+            raise ValueError(f"unknown rotary layout {layout!r} or scaling {scaling!r}")
+        c = cb_rope_config(head_dim, head_dim if rot_dim is None else rot_dim, ROPE_LAYOUTS[layout],
+                           ROPE_SCALINGS[scaling], base, factor, original_positions, beta_fast,
+                           beta_slow, low_freq_factor, high_freq_factor, amplitude)
+        self.c = cb_rope_plan()
+        _check(_lib.cb_rope_plan_init(ctypes.byref(c), ctypes.byref(self.c)))
+        self._p = ctypes.pointer(self.c)
+
+    @property
+    def head_dim(self) -> int:
+        return self.c.head_dim
+
+    @property
+    def rot_dim(self) -> int:
+        return self.c.rot_dim
+
+
+def _rope_rows(name, x, out, T, d, dtype):
+    """Pointers and token strides of [T, H, d] rows; a token's heads lie
+    packed, tokens may be further apart."""
+    for n, t in ((name, x), (name + "_out", out)):
+        if not t.is_cuda:
+            raise ValueError("tensors must live on the GPU (no CPU path)")
+        if t.dim() != 3 or t.shape != x.shape or t.shape[0] != T or t.shape[2] != d or t.dtype != dtype:
+            raise ValueError(f"{n} must be [tokens, heads, {d}] of one type and shape")
+        if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != d) or \
+                (T > 1 and t.stride(0) < t.shape[1] * d):
+            raise ValueError(f"{n}: the heads of a token must lie packed")
+    H = x.shape[1]
+    return (x.data_ptr(), out.data_ptr(), x.stride(0) if T > 1 else H * d,
+            out.stride(0) if T > 1 else H * d, H)
+
+
+def rope(q, k, positions, plan: RopePlan, *, q_out=None, k_out=None, inverse: bool = False,
+         stream=None):
+    """cb_rope: rotate q [T, Hq, D] and k [T, Hkv, D] (either may be None) by
+    ``positions`` int32 [T]; returns (q_out, k_out).  An output may be its
+    input.  ``inverse`` rotates back, which also turns gradients of the
+    outputs into gradients of the inputs."""
+    torch = _torch()
+    first = q if q is not None else k
+    if first is None:
+        raise ValueError("neither q nor k is given")
+    T, d = first.shape[0], plan.c.head_dim
+    a = cb_rope_args()
+    a.plan, a.num_tokens, a.dtype, a.inverse = plan._p, T, _dtype_code(first), int(bool(inverse))
+    if q is not None:
+        q_out = torch.empty_like(q) if q_out is None else q_out
+        a.q, a.q_out, a.q_stride, a.q_out_stride, a.num_q_heads = _rope_rows("q", q, q_out, T, d, first.dtype)
+    if k is not None:
+        k_out = torch.empty_like(k) if k_out is None else k_out
+        a.k, a.k_out, a.k_stride, a.k_out_stride, a.num_kv_heads = _rope_rows("k", k, k_out, T, d, first.dtype)
+    _need_i32("positions", positions, (T,))
+    _need_one_device(first, k, q_out, k_out, positions)
+    a.positions = positions.data_ptr()
+    _check(_lib.cb_rope(ctypes.byref(a), _stream_ptr(stream)))
+    return q_out, k_out
+
+
+def _need_q8(k_cache, v_cache, k_scales, v_scales):
+    """Shape (num_blocks, Hkv, block_size, D) of an 8-bit cache and the bytes
+    between two blocks' scales."""
+    torch = _torch()
+    _need_cuda(k_cache, v_cache)
+    if k_cache.dtype != torch.float8_e4m3fn or v_cache.dtype != torch.float8_e4m3fn:
+        raise TypeError("an 8-bit cache holds float8_e4m3fn codes")
+    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape:
+        raise ValueError("k_cache and v_cache must be [num_blocks, Hkv, block_size, D]")
+    nb, hkv, bs, d = k_cache.shape
+    for t in (k_scales, v_scales):
+        if not t.is_cuda:
+            raise ValueError("tensors must live on the GPU (no CPU path)")
+        if t.dtype != torch.uint8 or tuple(t.shape) != (nb, hkv):
+            raise ValueError("scales must be uint8 [num_blocks, Hkv]")
+    ss = max(k_scales.stride(0), hkv) if nb > 1 else hkv
+    for t in (k_scales, v_scales):
+        if (hkv > 1 and t.stride(1) != 1) or (nb > 1 and t.stride(0) != ss):
+            raise ValueError("scales: a block's must lie packed, at one stride for K and V")
+    _need_one_device(k_cache, v_cache, k_scales, v_scales)
+    return nb, hkv, bs, d, ss
+
+
+def kv_append_q8(k_new, v_new, slot_mapping, k_cache, v_cache, k_scales, v_scales, *,
+                 rope: Optional[RopePlan] = None, positions=None, q=None, q_out=None,
+                 error_word=None, stream=None):
+    """cb_kv_append_q8: k_new/v_new [T, Hkv, D] into an 8-bit cache --
+    ``k_cache``/``v_cache`` float8_e4m3fn [num_blocks, Hkv, 16, D],
+    ``k_scales``/``v_scales`` uint8 [num_blocks, Hkv].  With ``rope`` (and
+    ``positions`` int32 [T]) k is rotated first, and ``q`` [T, Hq, D]
+    (optional) into ``q_out``, which is returned."""
+    torch = _torch()
+    _need_cuda(k_new, v_new, slot_mapping)
+    nb, hkv, bs, d, ss = _need_q8(k_cache, v_cache, k_scales, v_scales)
+    T = slot_mapping.shape[0]
+    _need_i32("slot_mapping", slot_mapping, (T,))
+    for t in (k_new, v_new):
+        if tuple(t.shape) != (T, hkv, d) or t.dtype != k_new.dtype:
+            raise ValueError(f"k_new and v_new must be [{T}, {hkv}, {d}] of one type")
+    a = cb_append_q8_args(k_new.data_ptr(), v_new.data_ptr(), slot_mapping.data_ptr(), T,
+                          _dtype_code(k_new), k_cache.data_ptr(), v_cache.data_ptr(),
+                          k_scales.data_ptr(), v_scales.data_ptr(), ss, nb, hkv, d, bs)
+    if rope is not None:
+        if positions is None:
+            raise ValueError("rope needs positions")
+        _need_i32("positions", positions, (T,))
+        a.rope, a.positions = rope._p, positions.data_ptr()
+    elif q is not None or positions is not None:
+        raise ValueError("q and positions go with rope")
+    if q is not None:
+        q_out = torch.empty_like(q) if q_out is None else q_out
+        _need_cuda(q, q_out)
+        if q.dim() != 3 or q.shape[0] != T or q.shape[2] != d or q.dtype != k_new.dtype or \
+                q_out.shape != q.shape or q_out.dtype != q.dtype:
+            raise ValueError(f"q and q_out must be [{T}, Hq, {d}] of k_new's type")
+        a.q, a.q_out, a.num_q_heads = q.data_ptr(), q_out.data_ptr(), q.shape[1]
+    _need_one_device(k_cache, k_new, v_new, slot_mapping, positions, q, q_out, error_word)
+    if error_word is not None:
+        a.error_word = error_word.data_ptr()
+    _check(_lib.cb_kv_append_q8(ctypes.byref(a), _stream_ptr(stream)))
+    return q_out
+
+
+def paged_attention_q8(q, k_cache, v_cache, k_scales, v_scales, cu_seqlens_q, seq_lens,
+                       block_tables, *, num_decodes: int, max_q_len: int, max_seq_len: int,
+                       scale: float, workspace: Workspace, out=None, stream=None,
+                       sliding_window: int = 0, after_append: bool = False):
+    """cb_paged_attention_q8: ``paged_attention`` over an 8-bit cache (see
+    ``kv_append_q8``); q and out are bf16 or f32."""
+    torch = _torch()
+    _need_cuda(q)
+    nb, hkv, bs, d, ss = _need_q8(k_cache, v_cache, k_scales, v_scales)
+    if out is None:
+        out = torch.empty_like(q)
+    _need_cuda(out)
+    T, hq, _ = q.shape
+    R = seq_lens.shape[0]
+    if q.shape[2] != d or out.shape != q.shape or out.dtype != q.dtype:
+        raise ValueError(f"q and out must be [T, Hq, {d}] of one type")
+    _need_i32("cu_seqlens_q", cu_seqlens_q, (R + 1,))
+    _need_i32("seq_lens", seq_lens, (R,))
+    _need_i32("block_tables", block_tables, (R, block_tables.shape[-1]))
+    if R > workspace.max_reqs:
+        raise ValueError("workspace sized for fewer requests")
+    _need_one_device(q, out, k_cache, cu_seqlens_q, seq_lens, block_tables, workspace.buf)
+    a = cb_attention_args(q.data_ptr(), out.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+                          cu_seqlens_q.data_ptr(), seq_lens.data_ptr(), block_tables.data_ptr(),
+                          R, num_decodes, T, max_q_len, max_seq_len, nb, block_tables.shape[1],
+                          bs, hq, hkv, d, float(scale), _dtype_code(q), workspace.ptr,
+                          workspace.nbytes, int(sliding_window), int(bool(after_append)))
+    _check(_lib.cb_paged_attention_q8(ctypes.byref(a), k_scales.data_ptr(), v_scales.data_ptr(), ss,
+                                      _stream_ptr(stream)))
+    return out
+
+
 def inject_wait_timeout(wait_ns: int = 0, decode_item: int = -1, prefill_tile: int = -1) -> None:
     """cb_debug_inject_wait_timeout (test hook): shorten every bounded device
     wait of later launches to ``wait_ns`` (0 restores 1 s) and withhold the
@@ -619,5 +911,6 @@ def paged_attention_args(**kw) -> cb_attention_args:
 
 
 __all__ = ["Scheduler", "kv_append", "kv_swap", "validate_step", "paged_attention", "Workspace", "workspace_size",
-           "Executor",
+           "Executor", "step_tables", "trim_tables", "RopePlan", "rope", "kv_append_q8",
+           "paged_attention_q8",
            "CBError", "version", "library", "LIB_PATH"]

@@ -6,6 +6,7 @@
 // row-generic CUDA-core kernel.
 #include <cuda_runtime.h>
 
+#include "attention_common.h"
 #include "cb_error.h"
 #include "decode_launch.h"
 #include "device_utils.cuh"
@@ -17,51 +18,6 @@
 namespace cb {
 
 namespace {
-
-constexpr size_t kAlign = 256;
-inline size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
-
-struct WsLayout {
-  size_t header = 0, counters = 0, prefill = 0, part_ml = 0, part_acc = 0, total = 0;
-  int64_t slots = 0;  // decode partial slots
-};
-
-// Workspace regions.  The header, the decode split tickets and the prefill
-// region hold state that must read zero at the start of every call (each
-// call leaves them zero), so they sit at FIXED offsets that do not depend on
-// the call's sizes.  The split partials are scratch rewritten by every call,
-// sized by the call's decode rows.
-//   header words: [0] device error bits, [1] decode item counter
-//   counters: done[kPlanMax * kMaxKvHeads] (one ticket counter per
-//             (decode row, KV head) of a launch)
-constexpr int64_t kMaxKvHeads = 64;
-constexpr int kPlanMax = decode::kPlanMax;
-constexpr size_t kCounterWords = (size_t)kPlanMax * kMaxKvHeads;
-
-WsLayout ws_layout(int64_t num_reqs, int64_t Hq, int64_t Hkv, int64_t D) {
-  WsLayout w;
-  const int64_t rows = num_reqs < kPlanMax ? num_reqs : kPlanMax;
-  w.header = 0;
-  w.counters = kAlign;
-  w.prefill = w.counters + align_up(kCounterWords * 4);
-  w.part_ml = w.prefill + align_up(prefill_workspace_bytes(Hq, Hkv, D));
-  const size_t slots = (size_t)decode::partial_slots(rows, Hkv);
-  w.part_acc = w.part_ml + align_up(slots * Hq * 2 * 4);
-  w.total = w.part_acc + align_up(slots * Hq * D * 4);
-  w.slots = (int64_t)slots;
-  return w;
-}
-
-decode::Scratch decode_scratch(const cb_attention_args& a, const WsLayout& L) {
-  uint8_t* ws = static_cast<uint8_t*>(a.workspace);
-  decode::Scratch s{};
-  s.work_counter = reinterpret_cast<uint32_t*>(ws + L.header) + 1;
-  s.done = reinterpret_cast<uint32_t*>(ws + L.counters);
-  s.part_ml = reinterpret_cast<float*>(ws + L.part_ml);
-  s.part_acc = reinterpret_cast<float*>(ws + L.part_acc);
-  s.slots = L.slots;
-  return s;
-}
 
 template <typename T, int D>
 cb_status launch_simt_rows(const cb_attention_args& a, const WsLayout& L, int row_begin,
@@ -105,6 +61,36 @@ cb_status dispatch_simt(const cb_attention_args& a, const WsLayout& L, int row_b
 
 }  // namespace
 
+cb_status check_attention(const cb_attention_args& a) {
+  if (a.num_reqs < 0 || a.num_decodes < 0 || a.num_decodes > a.num_reqs || a.num_tokens < 0)
+    return fail(CB_ERR_INVALID_ARG, "bad row/token counts");
+  if (a.num_reqs == 0 || a.num_tokens == 0) return CB_OK;
+  if (!a.q || !a.out || !a.k_cache || !a.v_cache || !a.cu_seqlens_q || !a.seq_lens ||
+      !a.block_tables || !a.workspace)
+    return fail(CB_ERR_INVALID_ARG, "NULL pointer argument");
+  if (a.num_tokens < a.num_reqs) return fail(CB_ERR_INVALID_ARG, "num_tokens < num_reqs");
+  if (a.num_q_heads <= 0 || a.num_kv_heads <= 0 || a.num_q_heads % a.num_kv_heads != 0)
+    return fail(CB_ERR_INVALID_ARG, "num_q_heads must be a positive multiple of num_kv_heads");
+  if (a.num_kv_heads > kMaxKvHeads)
+    return fail(CB_ERR_UNSUPPORTED, "num_kv_heads > %d", (int)kMaxKvHeads);
+  if (a.block_size != 16) return fail(CB_ERR_UNSUPPORTED, "block_size must be 16");
+  if (a.head_dim != 64 && a.head_dim != 128) return fail(CB_ERR_UNSUPPORTED, "head_dim must be 64 or 128");
+  if (a.dtype != CB_DTYPE_F32 && a.dtype != CB_DTYPE_BF16) return fail(CB_ERR_INVALID_ARG, "unknown dtype");
+  if (a.num_blocks <= 0 || a.max_blocks_per_seq <= 0) return fail(CB_ERR_INVALID_ARG, "bad pool sizes");
+  if (a.sliding_window < 0) return fail(CB_ERR_INVALID_ARG, "sliding_window must be >= 0");
+  if (a.max_q_len < 1 || a.max_seq_len < a.max_q_len ||
+      (a.max_seq_len + a.block_size - 1) / a.block_size > a.max_blocks_per_seq)
+    return fail(CB_ERR_INVALID_ARG, "max_q_len / max_seq_len inconsistent with the block table");
+  const uintptr_t al = (uintptr_t)a.q | (uintptr_t)a.out | (uintptr_t)a.k_cache | (uintptr_t)a.v_cache;
+  if (al & 15u) return fail(CB_ERR_INVALID_ARG, "q/out/cache pointers must be 16-byte aligned");
+  if ((uintptr_t)a.workspace & (kAlign - 1))
+    return fail(CB_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+  const size_t need = ws_layout(a.num_reqs, a.num_q_heads, a.num_kv_heads, a.head_dim).total;
+  if (a.workspace_bytes < need)
+    return fail(CB_ERR_INVALID_ARG, "workspace too small: %zu < %zu", a.workspace_bytes, need);
+  return CB_OK;
+}
+
 }  // namespace cb
 
 using cb::fail;
@@ -141,32 +127,10 @@ extern "C" cb_status cb_paged_attention(const cb_attention_args* args, cb_stream
   if (!args) return fail(CB_ERR_INVALID_ARG, "args is NULL");
   const cb_attention_args& a = *args;
   cudaStream_t stream = (cudaStream_t)stream_;
-  if (a.num_reqs < 0 || a.num_decodes < 0 || a.num_decodes > a.num_reqs || a.num_tokens < 0)
-    return fail(CB_ERR_INVALID_ARG, "bad row/token counts");
+  cb_status cs = cb::check_attention(a);
+  if (cs != CB_OK) return cs;
   if (a.num_reqs == 0 || a.num_tokens == 0) return CB_OK;
-  if (!a.q || !a.out || !a.k_cache || !a.v_cache || !a.cu_seqlens_q || !a.seq_lens ||
-      !a.block_tables || !a.workspace)
-    return fail(CB_ERR_INVALID_ARG, "NULL pointer argument");
-  if (a.num_tokens < a.num_reqs) return fail(CB_ERR_INVALID_ARG, "num_tokens < num_reqs");
-  if (a.num_q_heads <= 0 || a.num_kv_heads <= 0 || a.num_q_heads % a.num_kv_heads != 0)
-    return fail(CB_ERR_INVALID_ARG, "num_q_heads must be a positive multiple of num_kv_heads");
-  if (a.num_kv_heads > cb::kMaxKvHeads)
-    return fail(CB_ERR_UNSUPPORTED, "num_kv_heads > %d", (int)cb::kMaxKvHeads);
-  if (a.block_size != 16) return fail(CB_ERR_UNSUPPORTED, "block_size must be 16");
-  if (a.head_dim != 64 && a.head_dim != 128) return fail(CB_ERR_UNSUPPORTED, "head_dim must be 64 or 128");
-  if (a.dtype != CB_DTYPE_F32 && a.dtype != CB_DTYPE_BF16) return fail(CB_ERR_INVALID_ARG, "unknown dtype");
-  if (a.num_blocks <= 0 || a.max_blocks_per_seq <= 0) return fail(CB_ERR_INVALID_ARG, "bad pool sizes");
-  if (a.sliding_window < 0) return fail(CB_ERR_INVALID_ARG, "sliding_window must be >= 0");
-  if (a.max_q_len < 1 || a.max_seq_len < a.max_q_len ||
-      (a.max_seq_len + a.block_size - 1) / a.block_size > a.max_blocks_per_seq)
-    return fail(CB_ERR_INVALID_ARG, "max_q_len / max_seq_len inconsistent with the block table");
-  const uintptr_t al = (uintptr_t)a.q | (uintptr_t)a.out | (uintptr_t)a.k_cache | (uintptr_t)a.v_cache;
-  if (al & 15u) return fail(CB_ERR_INVALID_ARG, "q/out/cache pointers must be 16-byte aligned");
-  if ((uintptr_t)a.workspace & (cb::kAlign - 1))
-    return fail(CB_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
   const cb::WsLayout L = cb::ws_layout(a.num_reqs, a.num_q_heads, a.num_kv_heads, a.head_dim);
-  if (a.workspace_bytes < L.total)
-    return fail(CB_ERR_INVALID_ARG, "workspace too small: %zu < %zu", a.workspace_bytes, L.total);
 
   if (cb::validate_enabled()) {
     cb_status vs = cb::validate_attention_call(a, stream);

@@ -115,18 +115,50 @@ cb_status validate_attention_call(const cb_attention_args& a, cudaStream_t strea
                           a.sliding_window);
 }
 
+namespace {
+
+cb_status check_slots(const std::vector<int32_t>& sm, int64_t slots) {
+  for (size_t t = 0; t < sm.size(); ++t)
+    if (sm[t] < -1 || sm[t] >= slots)
+      return fail(CB_ERR_INVALID_ARG, "validate: slot_mapping[%d] = %d outside [-1, %lld)", (int)t,
+                  sm[t], (long long)slots);
+  return CB_OK;
+}
+
+}  // namespace
+
 cb_status validate_append_call(const int32_t* slot_mapping, int32_t num_tokens, int32_t num_blocks,
                                int32_t block_size, cudaStream_t stream) {
   if (capturing(stream)) return CB_OK;
   std::vector<int32_t> sm;
   cb_status st = copy_back(&sm, slot_mapping, (size_t)num_tokens, stream);
   if (st != CB_OK) return st;
-  const int64_t slots = (int64_t)num_blocks * block_size;
-  for (int32_t t = 0; t < num_tokens; ++t)
-    if (sm[t] < -1 || sm[t] >= slots)
-      return fail(CB_ERR_INVALID_ARG, "validate: slot_mapping[%d] = %d outside [-1, %lld)", t, sm[t],
-                  (long long)slots);
+  return check_slots(sm, (int64_t)num_blocks * block_size);
+}
+
+cb_status validate_slot_runs(const int32_t* slots, int32_t num_tokens, int32_t num_blocks,
+                             int32_t block_size) {
+  std::vector<int32_t> last((size_t)num_blocks, -1);  // last token of each block so far
+  for (int32_t t = 0; t < num_tokens; ++t) {
+    if (slots[t] < 0) continue;
+    int32_t& prev = last[(size_t)(slots[t] / block_size)];
+    if (prev >= 0 && (prev != t - 1 || slots[prev] != slots[t] - 1))
+      return fail(CB_ERR_INVALID_ARG,
+                  "validate: slot_mapping[%d] = %d and [%d] = %d: the tokens of one block are no run",
+                  prev, slots[prev], t, slots[t]);
+    prev = t;
+  }
   return CB_OK;
+}
+
+cb_status validate_append_q8_call(const int32_t* slot_mapping, int32_t num_tokens,
+                                  int32_t num_blocks, int32_t block_size, cudaStream_t stream) {
+  if (capturing(stream)) return CB_OK;
+  std::vector<int32_t> sm;
+  cb_status st = copy_back(&sm, slot_mapping, (size_t)num_tokens, stream);
+  if (st == CB_OK) st = check_slots(sm, (int64_t)num_blocks * block_size);
+  if (st == CB_OK) st = validate_slot_runs(sm.data(), num_tokens, num_blocks, block_size);
+  return st;
 }
 
 }  // namespace cb

@@ -20,4 +20,13 @@ cb_status validate_attention_call(const cb_attention_args& a, cudaStream_t strea
 cb_status validate_append_call(const int32_t* slot_mapping, int32_t num_tokens,
                                int32_t num_blocks, int32_t block_size, cudaStream_t stream);
 
+// The same for cb_kv_append_q8's slot mapping, whose tokens of one block
+// have to be one run.
+cb_status validate_append_q8_call(const int32_t* slot_mapping, int32_t num_tokens,
+                                  int32_t num_blocks, int32_t block_size, cudaStream_t stream);
+
+// The run rule on host slots (range-checked already).
+cb_status validate_slot_runs(const int32_t* slots, int32_t num_tokens, int32_t num_blocks,
+                             int32_t block_size);
+
 }  // namespace cb
