@@ -264,7 +264,7 @@ extern "C" cb_status cb_rope_plan_init(const cb_rope_config* config, cb_rope_pla
       k = std::fmin(std::fmax(k, 0.0), 1.0);
       f *= k + (1.0 - k) / c.factor;
     }
-    out.turns[i] = (uint64_t)std::ldexp(f / two_pi, 64);  // f <= 1: below 2^62
+    out.turns[i] = (uint64_t)(std::ldexp(f / two_pi, 64) + 0.5);  // f <= 1: below 2^62
   }
   *plan = out;
   return CB_OK;
@@ -280,8 +280,8 @@ extern "C" cb_status cb_rope(const cb_rope_args* args, cb_stream_t stream) {
     return fail(CB_ERR_INVALID_ARG, "cb_rope: sizes must be positive");
   if (a.dtype != CB_DTYPE_F32 && a.dtype != CB_DTYPE_BF16)
     return fail(CB_ERR_INVALID_ARG, "cb_rope: unknown dtype");
-  if (!a.q && !a.k) return fail(CB_ERR_INVALID_ARG, "cb_rope: neither q nor k is given");
   if (a.num_tokens == 0) return CB_OK;
+  if (!a.q && !a.k) return fail(CB_ERR_INVALID_ARG, "cb_rope: neither q nor k is given");
   if (!a.positions || (a.q && !a.q_out) || (a.k && !a.k_out))
     return fail(CB_ERR_INVALID_ARG, "cb_rope: NULL pointer");
   if ((a.q && a.num_q_heads > (1 << 20)) || (a.k && a.num_kv_heads > (1 << 20)))

@@ -19,7 +19,64 @@ from typing import Optional
 
 import numpy as np
 
-from . import SWAP_MAX_POOLS, Workspace, kv_append, kv_swap, paged_attention
+from . import (SWAP_MAX_POOLS, Workspace, kv_append, kv_append_q8, kv_swap, paged_attention,
+               paged_attention_q8, rope, step_tables, trim_tables)
+
+
+def _make_caches(torch, num_layers, num_blocks, num_kv_heads, block_size, head_dim, dt, q8,
+                 zero_cache, device):
+    """(k_cache, v_cache, k_scales, v_scales) lists over the layers.  The
+    scales of an 8-bit cache (none otherwise) lie a multiple of 16 bytes
+    apart, so that whole blocks of them can be swapped; unwritten blocks have
+    the smallest scale."""
+    alloc = torch.zeros if zero_cache else torch.empty
+    shape = (num_blocks, num_kv_heads, block_size, head_dim)
+    mk = lambda: [alloc(shape, dtype=torch.uint8 if q8 else dt, device=device)
+                  for _ in range(num_layers)]
+    k, v = mk(), mk()
+    if not q8:
+        return k, v, [], []
+    codes = torch.float8_e4m3fn
+    wide = -(-num_kv_heads // 16) * 16
+    sc = lambda: [torch.full((num_blocks, wide), 127 - 40, dtype=torch.uint8, device=device)
+                  [:, :num_kv_heads] for _ in range(num_layers)]
+    return [t.view(codes) for t in k], [t.view(codes) for t in v], sc(), sc()
+
+
+def _is_q8(kv_dtype):
+    if kv_dtype not in (None, "e4m3"):
+        raise ValueError(f"unknown kv_dtype {kv_dtype!r}")
+    return kv_dtype == "e4m3"
+
+
+def _positions(cu, seq_lens, out):
+    """Positions of a step's tokens, from its host metadata, into out [T]."""
+    cu = np.asarray(cu, dtype=np.int64)
+    q = np.diff(cu)
+    first = np.asarray(seq_lens, dtype=np.int64) - q - cu[:-1]
+    out[:] = np.repeat(first, q) + np.arange(int(cu[-1]))
+
+
+def _layer(r, layer, q, k_new, v_new, cu, seq_lens, block_tables, slots, positions, *,
+           num_decodes, max_q_len, max_seq_len, out, after_append):
+    """One layer of a step of runner ``r``: rotate (if it has a rotary plan),
+    append, attend."""
+    kc, vc = r.k_cache[layer], r.v_cache[layer]
+    kw = dict(num_decodes=num_decodes, max_q_len=max_q_len, max_seq_len=max_seq_len,
+              scale=r.scale, workspace=r.workspace, out=out, sliding_window=r.sliding_window,
+              after_append=after_append)
+    if r.q8:
+        ks, vs = r.k_scales[layer], r.v_scales[layer]
+        if r.rope is not None:
+            q = kv_append_q8(k_new, v_new, slots, kc, vc, ks, vs, rope=r.rope,
+                             positions=positions, q=q)
+        else:
+            kv_append_q8(k_new, v_new, slots, kc, vc, ks, vs)
+        return paged_attention_q8(q, kc, vc, ks, vs, cu, seq_lens, block_tables, **kw)
+    if r.rope is not None:
+        q, k_new = rope(q, k_new, positions, r.rope)
+    kv_append(k_new, v_new, slots, kc, vc)
+    return paged_attention(q, kc, vc, cu, seq_lens, block_tables, **kw)
 
 
 class SwapPool:
@@ -38,17 +95,24 @@ class SwapPool:
     frees may be refilled by a swap-out of the same step.
     """
 
-    def __init__(self, k_cache, v_cache, swap_blocks: int, device="cuda"):
+    def __init__(self, k_cache, v_cache, swap_blocks: int, device="cuda", scales=()):
+        """``scales``: the scale arrays of 8-bit caches (views whose rows lie
+        a multiple of 16 bytes apart); they move with their blocks."""
         import torch
         self.torch = torch
         self.swap_blocks = int(swap_blocks)
-        shape = (self.swap_blocks,) + tuple(k_cache[0].shape[1:])
-        dt = k_cache[0].dtype
-        self.k = [torch.zeros(shape, dtype=dt, pin_memory=True) for _ in k_cache]
-        self.v = [torch.zeros(shape, dtype=dt, pin_memory=True) for _ in v_cache]
-        self._cache = list(k_cache) + list(v_cache)
-        self._pool = self.k + self.v
-        self.block_bytes = k_cache[0][0].numel() * k_cache[0].element_size()
+        # 8-bit codes are moved as bytes
+        raw = lambda t: t.view(torch.uint8) if t.element_size() == 1 else t
+        pin = lambda t: torch.zeros((self.swap_blocks,) + tuple(t.shape[1:]), dtype=t.dtype,
+                                    pin_memory=True)
+        caches = [raw(t) for t in list(k_cache) + list(v_cache)]
+        whole = [t.as_strided((t.shape[0], t.stride(0)), (t.stride(0), 1)) for t in scales]
+        # groups of pools of one block size: (cache side, host side)
+        self._groups = [(g, [pin(t) for t in g]) for g in (caches, whole) if g]
+        self.k = self._groups[0][1][:len(k_cache)]
+        self.v = self._groups[0][1][len(k_cache):]
+        self.block_bytes = caches[0][0].numel() * caches[0].element_size()
+        self._moved = sum(t[0].numel() * t.element_size() for t in caches + whole)
         cap = 4 * max(self.swap_blocks, 1)
         self._host = [torch.empty(cap, dtype=torch.int32, pin_memory=True) for _ in range(2)]
         self._copied = [None, None]
@@ -81,17 +145,16 @@ class SwapPool:
         ev.record()
         self._copied[b] = ev
         d = self._dev
-        for lo in range(0, len(self._cache), SWAP_MAX_POOLS):
-            hi = lo + SWAP_MAX_POOLS
-            if ni:
-                kv_swap(self._pool[lo:hi], self._cache[lo:hi], d[0:ni], d[ni:2 * ni],
-                        error_word=self.error_word)
-        for lo in range(0, len(self._cache), SWAP_MAX_POOLS):
-            hi = lo + SWAP_MAX_POOLS
-            if no:
-                kv_swap(self._cache[lo:hi], self._pool[lo:hi], d[2 * ni:2 * ni + no],
-                        d[2 * ni + no:n], error_word=self.error_word)
-        return (ni + no) * len(self._cache) * self.block_bytes
+        for n_pairs, out, first, second in ((ni, False, d[0:ni], d[ni:2 * ni]),
+                                            (no, True, d[2 * ni:2 * ni + no], d[2 * ni + no:n])):
+            if not n_pairs:
+                continue
+            for cache, host in self._groups:
+                for lo in range(0, len(cache), SWAP_MAX_POOLS):
+                    hi = lo + SWAP_MAX_POOLS
+                    src, dst = (cache, host) if out else (host, cache)
+                    kv_swap(src[lo:hi], dst[lo:hi], first, second, error_word=self.error_word)
+        return (ni + no) * self._moved
 
     def read_errors(self) -> int:
         return int(self.error_word.item())
@@ -109,14 +172,20 @@ class DeviceStep:
     block_tables: object
     slot_mapping: object
     h2d_bytes: int
+    positions: object = None    # [T], with a rotary plan or device tables
 
 
 class StepRunner:
+    """``kv_dtype`` "e4m3": the caches hold 8-bit codes with a scale for each
+    (block, KV head) (``kv_append_q8``, ``paged_attention_q8``) instead of
+    ``dtype``.  ``rope``: a ``RopePlan``; q and k are then given unrotated and
+    turn by their positions in each layer."""
+
     def __init__(self, *, num_blocks: int, num_q_heads: int, num_kv_heads: int, head_dim: int,
                  dtype: str, max_reqs: int, max_tokens: int, max_blocks_per_seq: int,
                  num_layers: int = 1, block_size: int = 16, device: str = "cuda",
                  scale: Optional[float] = None, zero_cache: bool = True, swap_blocks: int = 0,
-                 sliding_window: int = 0):
+                 sliding_window: int = 0, kv_dtype: Optional[str] = None, rope=None):
         import torch
         self.torch = torch
         self.dt = {"bf16": torch.bfloat16, "f32": torch.float32}[dtype]
@@ -127,13 +196,16 @@ class StepRunner:
         self.max_reqs, self.max_tokens = max_reqs, max_tokens
         self.W = max_blocks_per_seq
         self.scale = 1.0 / math.sqrt(head_dim) if scale is None else scale
-        alloc = torch.zeros if zero_cache else torch.empty
-        shape = (num_blocks, num_kv_heads, block_size, head_dim)
-        self.k_cache = [alloc(shape, dtype=self.dt, device=device) for _ in range(num_layers)]
-        self.v_cache = [alloc(shape, dtype=self.dt, device=device) for _ in range(num_layers)]
+        self.q8, self.rope = _is_q8(kv_dtype), rope
+        self.k_cache, self.v_cache, self.k_scales, self.v_scales = _make_caches(
+            torch, num_layers, num_blocks, num_kv_heads, block_size, head_dim, self.dt, self.q8,
+            zero_cache, device)
         self.workspace = Workspace(max_reqs, num_q_heads, num_kv_heads, head_dim, device=device)
-        self.swap = SwapPool(self.k_cache, self.v_cache, swap_blocks, device) if swap_blocks else None
+        self.swap = SwapPool(self.k_cache, self.v_cache, swap_blocks, device,
+                             self.k_scales + self.v_scales) if swap_blocks else None
         cap = (max_reqs + 1) + max_reqs + max_reqs * max_blocks_per_seq + max_tokens
+        if rope is not None:
+            cap += max_tokens
         # two pinned staging buffers, used in turn: a buffer is refilled only
         # after the copy that last read it has executed (its event), since
         # the host may run steps ahead of the device
@@ -154,8 +226,8 @@ class StepRunner:
 
     def _pack(self, step: dict, h: np.ndarray):
         """Write the step's metadata into the host int32 buffer ``h`` (one
-        packed run: cu_seqlens_q, seq_lens, block_tables, slot_mapping);
-        returns (words, offsets)."""
+        packed run: cu_seqlens_q, seq_lens, block_tables, slot_mapping, and
+        the positions with a rotary plan); returns (words, offsets)."""
         R, T = int(step["num_reqs"]), int(step["num_tokens"])
         if R > self.max_reqs or T > self.max_tokens:
             raise ValueError("step larger than the runner was sized for")
@@ -170,7 +242,10 @@ class StepRunner:
         h[o1:o2] = step["seq_lens"]
         h[o2:o3] = bt.reshape(-1)
         h[o3:o3 + T] = step["slot_mapping"]
-        return o3 + T, (o1, o2, o3)
+        if self.rope is None:
+            return o3 + T, (o1, o2, o3)
+        _positions(step["cu_seqlens_q"], step["seq_lens"], h[o3 + T:o3 + 2 * T])
+        return o3 + 2 * T, (o1, o2, o3)
 
     def _device_step(self, step: dict, d, n: int, offs) -> DeviceStep:
         R, T, W = int(step["num_reqs"]), int(step["num_tokens"]), self.W
@@ -179,7 +254,8 @@ class StepRunner:
                           else int(np.diff(step["cu_seqlens_q"]).max(initial=1)),
                           int(step["max_seq_len"]) if "max_seq_len" in step
                           else int(np.max(step["seq_lens"], initial=1)),
-                          d[0:R + 1], d[o1:o2], d[o2:o3].view(R, W), d[o3:o3 + T], 4 * n)
+                          d[0:R + 1], d[o1:o2], d[o2:o3].view(R, W), d[o3:o3 + T], 4 * n,
+                          None if self.rope is None else d[o3 + T:o3 + 2 * T])
 
     def upload(self, step: dict, stream=None) -> DeviceStep:
         """Queue the step's swaps, then copy its metadata to the device (one
@@ -201,13 +277,72 @@ class StepRunner:
     def run(self, ds: DeviceStep, q, k_new, v_new, layer: int = 0, out=None):
         """Append this step's K/V for ``layer`` and attend.  q [T, Hq, D],
         k_new/v_new [T, Hkv, D] on the device.  Returns out [T, Hq, D]."""
-        kc, vc = self.k_cache[layer], self.v_cache[layer]
-        kv_append(k_new, v_new, ds.slot_mapping, kc, vc)
-        return paged_attention(q, kc, vc, ds.cu_seqlens_q, ds.seq_lens, ds.block_tables,
-                               num_decodes=ds.num_decodes, max_q_len=ds.max_q_len,
-                               max_seq_len=ds.max_seq_len, scale=self.scale,
-                               workspace=self.workspace, out=out,
-                               sliding_window=self.sliding_window, after_append=True)
+        return _layer(self, layer, q, k_new, v_new, ds.cu_seqlens_q, ds.seq_lens, ds.block_tables,
+                      ds.slot_mapping, ds.positions, num_decodes=ds.num_decodes,
+                      max_q_len=ds.max_q_len, max_seq_len=ds.max_seq_len, out=out,
+                      after_append=True)
+
+
+class DeviceTables:
+    """Block tables, lengths and free blocks kept in device memory, for steps
+    whose metadata is built on the GPU (``cb_step_tables``) instead of by a
+    ``Scheduler``: the host gives query lengths, nothing is uploaded or read
+    back, and a whole step can be captured in a CUDA graph.
+
+    ``step(q_lens)`` appends q_lens[r] tokens to row r (an int32 device tensor
+    [max_reqs]; rows without tokens give 0) and returns a ``DeviceStep`` for
+    ``StepRunner.run``; its arrays are this object's and hold until the next
+    ``step``.  Rows [0, num_decodes) take at most one token each.  ``trim``
+    shortens rows (0: the request ended) and frees their blocks.  Rows that
+    do not fit are dropped and flagged in ``error_word``."""
+
+    def __init__(self, *, num_blocks: int, max_reqs: int, max_tokens: int,
+                 max_blocks_per_seq: int, block_size: int = 16, device: str = "cuda",
+                 free_list=None):
+        import torch
+        i32 = dict(dtype=torch.int32, device=device)
+        self.block_size, self.max_tokens = int(block_size), int(max_tokens)
+        self.cached_lens = torch.zeros(max_reqs, **i32)
+        self.block_tables = torch.full((max_reqs, max_blocks_per_seq), -1, **i32)
+        ids = np.arange(num_blocks) if free_list is None else np.asarray(free_list)
+        if sorted(ids.tolist()) != list(range(num_blocks)):
+            raise ValueError("free_list must hold every block id once")
+        self.free_ring = torch.tensor(ids.astype(np.int32), **i32)
+        self.free_state = torch.tensor([0, num_blocks], **i32)
+        self.cu_seqlens_q = torch.zeros(max_reqs + 1, **i32)
+        self.seq_lens = torch.zeros(max_reqs, **i32)
+        self.slot_mapping = torch.full((max_tokens,), -1, **i32)
+        self.positions = torch.zeros(max_tokens, **i32)
+        self.error_word = torch.zeros(1, **i32)
+
+    def step(self, q_lens, *, num_decodes: int, max_q_len: Optional[int] = None,
+             max_seq_len: Optional[int] = None, num_tokens: Optional[int] = None) -> DeviceStep:
+        """``max_q_len`` / ``max_seq_len``: host bounds on the rows' query and
+        sequence lengths (default: what the tables and tokens allow);
+        ``num_tokens``: how many tokens the step has room for (default: all
+        of max_tokens)."""
+        R, W = self.block_tables.shape
+        T = self.max_tokens if num_tokens is None else int(num_tokens)
+        longest = W * self.block_size
+        step_tables(q_lens, self.cached_lens, self.block_tables, self.free_ring, self.free_state,
+                    cu_seqlens_q=self.cu_seqlens_q, seq_lens=self.seq_lens,
+                    slot_mapping=self.slot_mapping[:T], positions=self.positions[:T],
+                    block_size=self.block_size, error_word=self.error_word)
+        most = 1 if num_decodes == R else min(T, longest)
+        return DeviceStep(R, T, num_decodes, most if max_q_len is None else int(max_q_len),
+                          longest if max_seq_len is None else int(max_seq_len),
+                          self.cu_seqlens_q, self.seq_lens, self.block_tables,
+                          self.slot_mapping[:T], 0, self.positions[:T])
+
+    def trim(self, keep_lens) -> None:
+        trim_tables(keep_lens, self.cached_lens, self.block_tables, self.free_ring,
+                    self.free_state, block_size=self.block_size, error_word=self.error_word)
+
+    def read_errors(self) -> int:
+        bits = int(self.error_word.item())
+        if bits:
+            self.error_word.zero_()
+        return bits
 
 
 class PipelinedStepRunner(StepRunner):
@@ -338,7 +473,7 @@ class GraphStepRunner:
                  dtype: str, max_reqs: int, max_tokens: int, max_blocks_per_seq: int,
                  num_layers: int = 1, block_size: int = 16, device: str = "cuda",
                  scale: Optional[float] = None, zero_cache: bool = True, swap_blocks: int = 0,
-                 sliding_window: int = 0):
+                 sliding_window: int = 0, kv_dtype: Optional[str] = None, rope=None):
         import torch
         self.torch = torch
         self.dt = {"bf16": torch.bfloat16, "f32": torch.float32}[dtype]
@@ -350,17 +485,20 @@ class GraphStepRunner:
         self.scale = 1.0 / math.sqrt(head_dim) if scale is None else scale
         self.R_cap = 2 * bucket(max_reqs)     # padded decode rows + padded prefill rows
         self.T_cap = bucket(max_tokens, 16)
-        alloc = torch.zeros if zero_cache else torch.empty
-        shape = (num_blocks, num_kv_heads, block_size, head_dim)
-        self.k_cache = [alloc(shape, dtype=self.dt, device=device) for _ in range(num_layers)]
-        self.v_cache = [alloc(shape, dtype=self.dt, device=device) for _ in range(num_layers)]
+        self.q8, self.rope = _is_q8(kv_dtype), rope
+        self.k_cache, self.v_cache, self.k_scales, self.v_scales = _make_caches(
+            torch, num_layers, num_blocks, num_kv_heads, block_size, head_dim, self.dt, self.q8,
+            zero_cache, device)
         self.workspace = Workspace(self.R_cap, num_q_heads, num_kv_heads, head_dim, device=device)
-        self.swap = SwapPool(self.k_cache, self.v_cache, swap_blocks, device) if swap_blocks else None
+        self.swap = SwapPool(self.k_cache, self.v_cache, swap_blocks, device,
+                             self.k_scales + self.v_scales) if swap_blocks else None
         mk = lambda h: [torch.zeros(self.T_cap, h, head_dim, dtype=self.dt, device=device)
                         for _ in range(num_layers)]
         self.q_buf, self.k_buf, self.v_buf = mk(num_q_heads), mk(num_kv_heads), mk(num_kv_heads)
         self.out_buf = mk(num_q_heads)
         cap = (self.R_cap + 1) + self.R_cap + self.R_cap * self.W + self.T_cap
+        if rope is not None:
+            cap += self.T_cap
         self._host = [torch.empty(cap, dtype=torch.int32, pin_memory=True) for _ in range(2)]
         self._copied = [None, None]
         self._turn = 0
@@ -412,6 +550,10 @@ class GraphStepRunner:
         h[o_bt:o_bt + Rb * W] = bt_p.reshape(-1)
         h[o_sm:o_sm + T] = step["slot_mapping"]
         h[o_sm + T:o_sm + Tb] = -1
+        if self.rope is not None:
+            _positions(step["cu_seqlens_q"], step["seq_lens"], h[n:n + T])
+            h[n + T:n + Tb] = 0
+            n += Tb
         self._dev[:n].copy_(self._host[b][:n], non_blocking=True)
         ev = self.torch.cuda.Event()
         ev.record()
@@ -425,17 +567,16 @@ class GraphStepRunner:
         d = self._dev
         cu, sl = d[0:Rb + 1], d[Rb + 1:2 * Rb + 1]
         bt = d[2 * Rb + 1:2 * Rb + 1 + Rb * W].view(Rb, W)
-        sm = d[2 * Rb + 1 + Rb * W:2 * Rb + 1 + Rb * W + Tb]
+        o_sm = 2 * Rb + 1 + Rb * W
+        sm, pos = d[o_sm:o_sm + Tb], None if self.rope is None else d[o_sm + Tb:o_sm + 2 * Tb]
         for layer in range(self.L):
-            kc, vc = self.k_cache[layer], self.v_cache[layer]
-            kv_append(self.k_buf[layer][:Tb], self.v_buf[layer][:Tb], sm, kc, vc)
             # a chunk's bucket may pass the longest sequence the table spans;
             # no real chunk does
-            paged_attention(self.q_buf[layer][:Tb], kc, vc, cu, sl, bt, num_decodes=ndb,
-                            max_q_len=min(max(mqb, 1), W * self.block_size),
-                            max_seq_len=W * self.block_size,
-                            scale=self.scale, workspace=self.workspace,
-                            out=self.out_buf[layer][:Tb], sliding_window=self.sliding_window)
+            _layer(self, layer, self.q_buf[layer][:Tb], self.k_buf[layer][:Tb],
+                   self.v_buf[layer][:Tb], cu, sl, bt, sm, pos, num_decodes=ndb,
+                   max_q_len=min(max(mqb, 1), W * self.block_size),
+                   max_seq_len=W * self.block_size, out=self.out_buf[layer][:Tb],
+                   after_append=False)
 
     def run(self, key):
         """Run the step last prepared (key from prepare)."""
