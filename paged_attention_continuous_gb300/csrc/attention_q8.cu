@@ -8,6 +8,7 @@
 
 #include "attention_common.h"
 #include "cb_error.h"
+#include "decode_q8.h"
 #include "q8.cuh"
 #include "rope.cuh"
 #include "validate.h"
@@ -142,6 +143,18 @@ extern "C" cb_status cb_paged_attention_q8(const cb_attention_args* args, const 
     st = cb::validate_attention_call(a, stream);
     if (st != CB_OK) return st;
   }
+  // Decode rows run the split-KV kernel; the others, and decodes with more
+  // heads than it takes, the row kernel.
+  int done = 0;  // rows [0, done) need nothing more
+  if (a.num_decodes > 0) {
+    const cb::WsLayout L = cb::ws_layout(a.num_reqs, a.num_q_heads, a.num_kv_heads, a.head_dim);
+    st = cb::decode_q8::dispatch(a, k_scales, v_scales, scale_stride, cb::decode_scratch(a, L),
+                                 static_cast<uint32_t*>(a.workspace), stream,
+                                 a.after_append ? cb::decode::After::kAppend : cb::decode::After::kStream);
+    if (st != CB_OK && st != CB_ERR_UNSUPPORTED) return st;
+    if (st == CB_OK) done = a.num_decodes;
+  }
+  if (done == a.num_reqs) return CB_OK;
   cb::q8::RowsParams p{};
   p.q = a.q;
   p.out = a.out;
@@ -153,7 +166,7 @@ extern "C" cb_status cb_paged_attention_q8(const cb_attention_args* args, const 
   p.cu_seqlens_q = a.cu_seqlens_q;
   p.seq_lens = a.seq_lens;
   p.block_tables = a.block_tables;
-  p.row_begin = 0;
+  p.row_begin = done;
   p.row_end = a.num_reqs;
   p.num_rows = a.num_reqs;
   p.num_tokens = a.num_tokens;

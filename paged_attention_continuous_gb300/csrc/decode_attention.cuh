@@ -63,16 +63,11 @@
 
 #include "decode_launch.h"
 #include "device_utils.cuh"
+#include "mma_utils.cuh"
+#include "split_plan.cuh"
 
 namespace cb {
 namespace decode {
-
-constexpr int kPageTokens = 16;
-constexpr int kTailDiv = 8;         // the last 1/kTailDiv of each row's pages: phase B
-constexpr int kMinSplitPages = 8;   // phase-A split size floor
-// shared memory of the plan: split-count prefixes of both phases, and each
-// row's sequence length (0 for a row that is skipped) and query token
-constexpr int kPlanSmemBytes = (2 * (kPlanMax + 1) + 2 * kPlanMax) * (int)sizeof(int32_t);
 
 struct Params {
   // bf16 caches: 2-D views [num_blocks * Hkv * 16 rows][D] of K and V, box
@@ -108,28 +103,6 @@ struct Params {
   int32_t withhold_item;   // test hook: the item with this global index
                            // never gets its first page's copies (-1: none)
 };
-
-// How a row of `pages` pages is cut, given the launch-wide split sizes spa
-// (phase A) and spb (phase B): phase A covers pages [0, bp) in na full
-// splits of spa pages, na = floor(leading (1 - 1/kTailDiv) of the row / spa);
-// phase B covers the rest, [bp, pages), in nb splits of spb pages (the last
-// one shorter).
-struct RowSplit {
-  int na, bp, nb;
-};
-
-// First key and first page a decode row of length L reads (window W, 0 = all).
-__device__ __forceinline__ int first_key(int L, int W) { return W > 0 && L > W ? L - W : 0; }
-__device__ __forceinline__ int first_page(int L, int W) { return first_key(L, W) / kPageTokens; }
-
-__device__ __forceinline__ RowSplit row_split(int pages, int spa, int spb) {
-  RowSplit s;
-  const int big = pages - pages / kTailDiv;
-  s.na = big / spa;
-  s.bp = s.na * spa;
-  s.nb = (pages - s.bp + spb - 1) / spb;
-  return s;
-}
 
 // CUDA-core geometry (fp32 caches)
 template <typename T, int D, int G>
@@ -185,43 +158,6 @@ constexpr size_t smem_bytes() {
   return sizeof(WarpSmem<T, D, G, kStages>) * kWarps + kPlanSmemBytes + 1024;
 }
 
-// ---- matrix-instruction helpers -------------------------------------------
-__device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t (&r)[4]) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
-__device__ __forceinline__ void ldsm_x4_trans(uint32_t addr, uint32_t (&r)[4]) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
-// transpose of an 8x8 b16 matrix held one 32-bit pair per lane
-__device__ __forceinline__ uint32_t movmatrix_trans(uint32_t a) {
-  uint32_t d;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
-  return d;
-}
-// c += a . b, m16n8k16, bf16 inputs, fp32 accumulate
-__device__ __forceinline__ void mma_bf16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
-                                         uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-      "{%8,%9}, {%0,%1,%2,%3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-// 2-D TMA box load with an L2 eviction hint, completion on an mbarrier
-__device__ __forceinline__ void tma_load_2d_hint(void* smem_dst, const CUtensorMap* tmap, int32_t x,
-                                                 int32_t y, uint64_t* bar, uint64_t pol) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint "
-      "[%0], [%1, {%2, %3}], [%4], %5;" ::"r"(smem_addr(smem_dst)),
-      "l"(tmap), "r"(x), "r"(y), "r"(smem_addr(bar)), "l"(pol)
-      : "memory");
-}
 // byte offset of 16-byte chunk `gc` (0 .. D/8-1) of page row `t` in a page
 // landed as 64-dim boxes of 16 rows x 128 bytes with the 128-byte swizzle
 __device__ __forceinline__ uint32_t swz_off(int t, int gc) {
@@ -367,125 +303,24 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_kernel(const __grid_con
   int32_t* plan_b = plan_a + (kPlanMax + 1);                                  // [num_rows + 1]
   int32_t* row_len = plan_b + (kPlanMax + 1);                                 // [num_rows]
   int32_t* row_tok = row_len + kPlanMax;                                      // [num_rows]
-  __shared__ int32_t s_red[kWarps];
-  __shared__ int32_t s_red2[kWarps];
-  __shared__ int32_t s_spa, s_spb;
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  const int nthreads = kWarps * 32;
   const int Hkv = p.num_kv_heads;
   const int Hq = p.num_q_heads;
   const int W = p.max_blocks_per_seq;
   const int win = kWindow ? p.window : 0;
 
   // ---- plan: pages per row -> split sizes -> prefixes of split counts -----
-  // Rows are checked once here and kept in shared memory; a row that fails a
-  // check gets length 0 (no items) and its error bit.
-  int64_t my_pages = 0;
-  for (int i = threadIdx.x; i < p.num_rows; i += nthreads) {
-    const int r = p.row_begin + i;
-    int L = p.seq_lens[r];
-    const int q0 = p.cu_seqlens_q[r];
-    const int q1 = p.cu_seqlens_q[r + 1];
-    int pages = (L + kPageTokens - 1) / kPageTokens;
-    if (L == 0 && q1 == q0) {
-      // a padding row (no query, no context): nothing to do
-    } else {
-      if (L < 1 || pages > W) {
-        L = 0;
-        if (blockIdx.x == 0) set_error(p.error_word, CB_DEVERR_SEQ_RANGE);
-      }
-      if (q1 - q0 != 1 || q0 < 0 || q0 >= p.num_tokens) {
-        L = 0;
-        if (blockIdx.x == 0) set_error(p.error_word, CB_DEVERR_DECODE_QLEN);
-      }
-    }
-    pages = (L + kPageTokens - 1) / kPageTokens - first_page(L, win);
-    row_len[i] = L;
-    row_tok[i] = q0;
-    my_pages += pages;
-  }
-  for (int o = 16; o > 0; o >>= 1) my_pages += __shfl_xor_sync(0xffffffffu, my_pages, o);
-  if (lane == 0) s_red[warp] = (int32_t)(my_pages < 0x3fffffff ? my_pages : 0x3fffffff);
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    int64_t tot = 0;
-    for (int w = 0; w < kWarps; ++w) tot += s_red[w];
-    const int64_t units = tot * Hkv;
-    const int64_t units_b = units / kTailDiv;
-    const int64_t workers = (int64_t)gridDim.x * kWarps;
-    // beside a prefill grid (pdl_mode 2) the CTAs start at different times
-    // and draw every item from the counter: smaller items keep their finish
-    // together
-    const int64_t items_a = p.pdl_mode == 2 ? kItemsABeside : kItemsA;
-    int64_t spa = (units - units_b + workers * items_a - 1) / (workers * items_a);
-    int64_t spb = (units_b + workers * kItemsB - 1) / (workers * kItemsB);
-    if (spa < kMinSplitPages) spa = kMinSplitPages;
-    if (spb < 1) spb = 1;
-    s_spa = (int32_t)(spa < (1 << 20) ? spa : (1 << 20));
-    s_spb = (int32_t)(spb < (1 << 20) ? spb : (1 << 20));
-  }
-  __syncthreads();
-  int spa0 = s_spa, spb0 = s_spb;
-  // per row split counts of both phases and their prefixes (serial segments
-  // per thread + a block scan of the segment sums); if the splits exceed the
-  // partial slots, double both split sizes and plan again
-  for (int attempt = 0;; ++attempt) {
-    const int seg = (p.num_rows + nthreads - 1) / nthreads;
-    const int b = threadIdx.x * seg;
-    const int e = min(b + seg, p.num_rows);
-    int sum_a = 0, sum_b = 0;
-    for (int i = b; i < e; ++i) {
-      const int Li = row_len[i];
-      const RowSplit rs =
-          row_split((Li + kPageTokens - 1) / kPageTokens - first_page(Li, win), spa0, spb0);
-      const int na = rs.na, nb = rs.nb;
-      plan_a[i + 1] = na;
-      plan_b[i + 1] = nb;
-      sum_a += na;
-      sum_b += nb;
-    }
-    int inc_a = sum_a, inc_b = sum_b;
-    for (int o = 1; o < 32; o <<= 1) {
-      const int va = __shfl_up_sync(0xffffffffu, inc_a, o);
-      const int vb = __shfl_up_sync(0xffffffffu, inc_b, o);
-      if (lane >= o) {
-        inc_a += va;
-        inc_b += vb;
-      }
-    }
-    if (lane == 31) {
-      s_red[warp] = inc_a;
-      s_red2[warp] = inc_b;
-    }
-    __syncthreads();
-    int off_a = 0, off_b = 0;
-    for (int w = 0; w < warp; ++w) {
-      off_a += s_red[w];
-      off_b += s_red2[w];
-    }
-    int run_a = off_a + inc_a - sum_a, run_b = off_b + inc_b - sum_b;
-    if (threadIdx.x == 0) {
-      plan_a[0] = 0;
-      plan_b[0] = 0;
-    }
-    for (int i = b; i < e; ++i) {
-      run_a += plan_a[i + 1];
-      run_b += plan_b[i + 1];
-      plan_a[i + 1] = run_a;
-      plan_b[i + 1] = run_b;
-    }
-    __syncthreads();
-    if (plan_a[p.num_rows] + plan_b[p.num_rows] <= p.max_slots || attempt >= 40) break;
-    if (spa0 < (1 << 29)) spa0 *= 2;
-    if (spb0 < (1 << 29)) spb0 *= 2;
-    __syncthreads();  // everyone has read the totals before they are rewritten
-  }
-  // unreachable with max_slots >= 2 * num_rows; refuse rather than overrun
-  const bool plan_ok = plan_a[p.num_rows] + plan_b[p.num_rows] <= p.max_slots &&
-                       (int64_t)(plan_a[p.num_rows] + plan_b[p.num_rows]) * Hkv < (1 << 26);
-  if (!plan_ok && blockIdx.x == 0 && threadIdx.x == 0) set_error(p.error_word, CB_DEVERR_PLAN);
+  // beside a prefill grid (pdl_mode 2) the CTAs start at different times and
+  // draw every item from the counter: smaller items keep their finish
+  // together
+  const SplitPlan plan = plan_splits<kWarps>(
+      PlanRows{p.seq_lens, p.cu_seqlens_q, p.row_begin, p.num_rows, p.num_tokens, W, Hkv, win,
+               p.max_slots, p.pdl_mode == 2 ? kItemsABeside : kItemsA, p.error_word},
+      kWarps, plan_a, plan_b, row_len, row_tok);
+  const int spa0 = plan.spa, spb0 = plan.spb;
+  const bool plan_ok = plan.ok;
   const int num_a = plan_a[p.num_rows];
   const int num_b = plan_b[p.num_rows];
   const int total_items = plan_ok ? (num_a + num_b) * Hkv : 0;

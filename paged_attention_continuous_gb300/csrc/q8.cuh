@@ -49,6 +49,16 @@ __device__ __forceinline__ uint32_t halves2(uint16_t codes) {
   return r;
 }
 
+// Four codes to two pairs of halves.
+__device__ __forceinline__ void halves4(uint32_t codes, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 a, b;\n\t"
+      "mov.b32 {a, b}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(codes));
+}
+
 // Two halves to codes, to nearest even.
 __device__ __forceinline__ uint16_t codes_of_halves(uint32_t h) {
   uint16_t r;

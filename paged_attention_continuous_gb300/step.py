@@ -95,6 +95,8 @@ class SwapPool:
     frees may be refilled by a swap-out of the same step.
     """
 
+    _scales, _scale_pool = (), ()
+
     def __init__(self, k_cache, v_cache, swap_blocks: int, device="cuda", scales=()):
         """``scales``: the scale arrays of 8-bit caches (views whose rows lie
         a multiple of 16 bytes apart); they move with their blocks."""
@@ -105,14 +107,12 @@ class SwapPool:
         raw = lambda t: t.view(torch.uint8) if t.element_size() == 1 else t
         pin = lambda t: torch.zeros((self.swap_blocks,) + tuple(t.shape[1:]), dtype=t.dtype,
                                     pin_memory=True)
-        caches = [raw(t) for t in list(k_cache) + list(v_cache)]
-        whole = [t.as_strided((t.shape[0], t.stride(0)), (t.stride(0), 1)) for t in scales]
-        # groups of pools of one block size: (cache side, host side)
-        self._groups = [(g, [pin(t) for t in g]) for g in (caches, whole) if g]
-        self.k = self._groups[0][1][:len(k_cache)]
-        self.v = self._groups[0][1][len(k_cache):]
-        self.block_bytes = caches[0][0].numel() * caches[0].element_size()
-        self._moved = sum(t[0].numel() * t.element_size() for t in caches + whole)
+        self._cache = [raw(t) for t in list(k_cache) + list(v_cache)]
+        self._pool = [pin(t) for t in self._cache]
+        self.k, self.v = self._pool[:len(k_cache)], self._pool[len(k_cache):]
+        self.block_bytes = k_cache[0][0].numel() * k_cache[0].element_size()
+        self._scales = [t.as_strided((t.shape[0], t.stride(0)), (t.stride(0), 1)) for t in scales]
+        self._scale_pool = [pin(t) for t in self._scales]
         cap = 4 * max(self.swap_blocks, 1)
         self._host = [torch.empty(cap, dtype=torch.int32, pin_memory=True) for _ in range(2)]
         self._copied = [None, None]
@@ -145,16 +145,16 @@ class SwapPool:
         ev.record()
         self._copied[b] = ev
         d = self._dev
+        # pools of one block size go in one call: codes (or values), scales
+        groups = [(self._cache, self._pool), (self._scales, self._scale_pool)]
         for n_pairs, out, first, second in ((ni, False, d[0:ni], d[ni:2 * ni]),
                                             (no, True, d[2 * ni:2 * ni + no], d[2 * ni + no:n])):
-            if not n_pairs:
-                continue
-            for cache, host in self._groups:
+            for cache, host in groups if n_pairs else ():
                 for lo in range(0, len(cache), SWAP_MAX_POOLS):
                     hi = lo + SWAP_MAX_POOLS
                     src, dst = (cache, host) if out else (host, cache)
                     kv_swap(src[lo:hi], dst[lo:hi], first, second, error_word=self.error_word)
-        return (ni + no) * self._moved
+        return (ni + no) * (len(self._cache) * self.block_bytes + sum(t.shape[1] for t in self._scales))
 
     def read_errors(self) -> int:
         return int(self.error_word.item())
@@ -180,6 +180,8 @@ class StepRunner:
     (block, KV head) (``kv_append_q8``, ``paged_attention_q8``) instead of
     ``dtype``.  ``rope``: a ``RopePlan``; q and k are then given unrotated and
     turn by their positions in each layer."""
+
+    q8, rope = False, None
 
     def __init__(self, *, num_blocks: int, num_q_heads: int, num_kv_heads: int, head_dim: int,
                  dtype: str, max_reqs: int, max_tokens: int, max_blocks_per_seq: int,
@@ -467,7 +469,10 @@ class GraphStepRunner:
     returns the bucket; the caller writes the step's q/k/v rows into
     ``q_buf[layer][:T]``, ``k_buf[layer][:T]``, ``v_buf[layer][:T]``; ``run(key)``
     replays the graph; the outputs are ``out_buf[layer][:T]``.
+    ``kv_dtype`` and ``rope`` are ``StepRunner``'s.
     """
+
+    q8, rope = False, None
 
     def __init__(self, *, num_blocks: int, num_q_heads: int, num_kv_heads: int, head_dim: int,
                  dtype: str, max_reqs: int, max_tokens: int, max_blocks_per_seq: int,
