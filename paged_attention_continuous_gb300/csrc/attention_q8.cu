@@ -9,6 +9,8 @@
 #include "attention_common.h"
 #include "cb_error.h"
 #include "decode_q8.h"
+#include "launch_common.h"
+#include "prefill_q8.h"
 #include "q8.cuh"
 #include "rope.cuh"
 #include "validate.h"
@@ -143,18 +145,48 @@ extern "C" cb_status cb_paged_attention_q8(const cb_attention_args* args, const 
     st = cb::validate_attention_call(a, stream);
     if (st != CB_OK) return st;
   }
-  // Decode rows run the split-KV kernel; the others, and decodes with more
-  // heads than it takes, the row kernel.
-  int done = 0;  // rows [0, done) need nothing more
-  if (a.num_decodes > 0) {
+  // Decode rows run the split-KV kernel, the others the prefill kernel; what
+  // those two do not take (KV heads shared by very many query heads) runs
+  // the row kernel.  Their order is cb_paged_attention's: decodes first,
+  // unless the prefill grid leaves SMs idle for its whole, long run.
+  using cb::decode::After;
+  uint32_t* ew = static_cast<uint32_t*>(a.workspace);
+  const int nd = a.num_decodes;
+  auto run_decode = [&](After after) {
     const cb::WsLayout L = cb::ws_layout(a.num_reqs, a.num_q_heads, a.num_kv_heads, a.head_dim);
-    st = cb::decode_q8::dispatch(a, k_scales, v_scales, scale_stride, cb::decode_scratch(a, L),
-                                 static_cast<uint32_t*>(a.workspace), stream,
-                                 a.after_append ? cb::decode::After::kAppend : cb::decode::After::kStream);
+    return cb::decode_q8::dispatch(a, k_scales, v_scales, scale_stride, cb::decode_scratch(a, L), ew, stream, after);
+  };
+  auto run_prefill = [&](bool overlap) {
+    return cb::prefill_q8::launch(a, k_scales, v_scales, scale_stride, ew, stream, overlap);
+  };
+  bool decodes_left = nd > 0, prefills_left = nd < a.num_reqs;
+  const int64_t ctas = cb::prefill_q8::ctas(a);
+  if (decodes_left && ctas > 0 && a.max_seq_len >= 16384 && ctas + 16 <= cb::sm_count_current_device()) {
+    st = run_prefill(false);
     if (st != CB_OK && st != CB_ERR_UNSUPPORTED) return st;
-    if (st == CB_OK) done = a.num_decodes;
+    if (st == CB_OK) {
+      prefills_left = false;
+      st = run_decode(After::kPrefill);
+      if (st != CB_OK && st != CB_ERR_UNSUPPORTED) return st;
+      decodes_left = st != CB_OK;
+    }
   }
-  if (done == a.num_reqs) return CB_OK;
+  bool decode_before = false;
+  if (decodes_left && prefills_left) {
+    st = run_decode(a.after_append ? After::kAppend : After::kStream);
+    if (st != CB_OK && st != CB_ERR_UNSUPPORTED) return st;
+    decode_before = st == CB_OK;
+    decodes_left = !decode_before;
+  } else if (decodes_left && nd == a.num_reqs) {
+    st = run_decode(a.after_append ? After::kAppend : After::kStream);
+    if (st != CB_ERR_UNSUPPORTED) return st;
+  }
+  if (prefills_left) {
+    st = run_prefill(decode_before);
+    if (st != CB_OK && st != CB_ERR_UNSUPPORTED) return st;
+    prefills_left = st != CB_OK;
+  }
+  if (!decodes_left && !prefills_left) return CB_OK;
   cb::q8::RowsParams p{};
   p.q = a.q;
   p.out = a.out;
@@ -166,8 +198,8 @@ extern "C" cb_status cb_paged_attention_q8(const cb_attention_args* args, const 
   p.cu_seqlens_q = a.cu_seqlens_q;
   p.seq_lens = a.seq_lens;
   p.block_tables = a.block_tables;
-  p.row_begin = done;
-  p.row_end = a.num_reqs;
+  p.row_begin = decodes_left ? 0 : nd;
+  p.row_end = prefills_left ? a.num_reqs : nd;
   p.num_rows = a.num_reqs;
   p.num_tokens = a.num_tokens;
   p.num_blocks = a.num_blocks;

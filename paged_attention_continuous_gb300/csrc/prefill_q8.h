@@ -1,0 +1,25 @@
+// Launch of the prefill-chunk kernel over the 8-bit cache.
+#pragma once
+
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "../../include/cb.h"
+
+namespace cb {
+namespace prefill_q8 {
+
+// CTAs of the prefill rows of `a` (an upper bound; 0 without prefill rows or
+// where this kernel does not take them).
+int64_t ctas(const cb_attention_args& a);
+
+// Rows [num_decodes, num_reqs) of `a`.  Returns CB_ERR_UNSUPPORTED (without a
+// message) for more than 128 query heads to a KV head.  overlap_previous: the
+// kernel queued just before on `stream` is the decode kernel of the same
+// call, which this grid may overlap (programmatic stream serialization).
+cb_status launch(const cb_attention_args& a, const uint8_t* k_scales, const uint8_t* v_scales,
+                 int64_t scale_stride, uint32_t* error_word, cudaStream_t stream,
+                 bool overlap_previous);
+
+}  // namespace prefill_q8
+}  // namespace cb
