@@ -11,11 +11,15 @@
 // FLOP for each query head and visible key); the codes ask for what the
 // 16-bit kernel does not have:
 //
-//   * Four converter warps read the pages' codes from global memory into
-//     registers, a tile ahead, expand them to halves (every e4m3 number is
-//     one exactly: one conversion for two codes) and store them in the
-//     swizzled layout that the matrix instructions read.  No raw codes pass
-//     through shared memory.
+//   * Two producer warps gather the pages' codes through the block table (one
+//     TMA box of 16 rows per page) into one raw tile each for K and V.  Four
+//     converter warps take a raw tile into registers, which frees it for the
+//     next tile's copies at once, expand it to halves (every e4m3 number is
+//     one exactly: one conversion for two codes) and store those in the
+//     swizzled layout that the matrix instructions read.  (Reading the codes
+//     from global memory into the converters' registers instead was 2.3 times
+//     slower: with 227 KB of shared memory in use the L1 holds too few
+//     outstanding loads.)
 //   * Both products are kind::f16 with half operands: Q rows are scaled by a
 //     power of two to the halves' range (so bfloat16 queries are halves
 //     exactly; elements under 2^-29 of the row's largest lose bits).
@@ -23,15 +27,15 @@
 //     2^ek times the row's; a weight is 2^(x + ev - m) with x the score in
 //     powers of two, so that weight times code is the value's part, and the
 //     running reference m is over x + ev.  The sum of weights adds each
-//     block's sum times 2^-ev.  Weights are halves: scores go through
-//     ex2.f16x2 (an exponent in [-8, 8] is off by 2^-9 at most), 8 times
-//     finer than bfloat16 exponents for the same instructions.  A weight
-//     below 2^-24 is zero; a block whose values are more than 2^4 smaller
-//     than the largest so far gets its part of the sum from float32
-//     exponentials instead, where x counts and x + ev does not.
+//     block's sum times 2^-ev, in float32 and from the unrounded weights, so
+//     that a block of small values counts in it in full; the weights
+//     themselves are rounded to halves (2^7 at the reference, 2^15 at most;
+//     below 2^-25 they are zero, 2^-32 of the largest).  Exponentials are
+//     float32: the unit takes 4 cycles a warp for them and 8 for a pair of
+//     halves or bfloat16s, so the packed forms only lose bits.
 //   * float32 queries: Q and the weights are split into two halves each (22
 //     bits), one query tile per CTA (the second tile's place holds the low
-//     halves), float32 exponentials.
+//     halves).
 //   * A value code that is NaN must not reach rows that do not see its key
 //     (weight 0 times NaN is NaN): in tiles that some row of the CTA sees only
 //     in part, converters store such codes as 0 and note the first and last
@@ -41,11 +45,13 @@
 // written over S_t as half pairs and read from there as the A operand.
 //
 // Warp roles (512 threads, registers redistributed):
-//   0-3 / 4-7  softmax of query tile 0 / 1 (thread = row): 184 registers
-//   10, 11     MMA issuers of the two tiles (8, 9 idle; 10 owns TMEM): 48
-//   12-15      converters: 96
+//   0-3 / 4-7  softmax of query tile 0 / 1 (thread = row): 192 registers
+//   8, 9       producers of raw K and V tiles: 48
+//   10, 11     MMA issuers of the two tiles (10 owns TMEM): 48
+//   12-15      converters: 80
 // Per KV tile j an issuer queues P.V(j-1) and then Q.K(j).  Every wait is
 // bounded (CB_DEVERR_TIMEOUT).
+#include <cuda.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
@@ -60,6 +66,7 @@
 #include "q8.cuh"
 #include "rope.cuh"
 #include "tcgen05.cuh"
+#include "tensor_map.h"
 
 namespace cb {
 namespace prefill_q8 {
@@ -68,35 +75,38 @@ constexpr int kBM = 128;            // query rows per tile
 constexpr int kBN = 128;            // keys per KV tile
 constexpr int kPage = 16;
 constexpr int kPages = kBN / kPage; // blocks of a KV tile
-constexpr int kStagesK = 3;
-constexpr int kStagesV = 2;
-constexpr int kScaleSlots = 8;      // tiles whose scales are kept (see below)
+constexpr int kStages = 2;          // tiles of K, and of V, as halves
+constexpr int kScaleSlots = 4;      // tiles whose scales are kept (see Bars)
 constexpr int kMmaWarp = 10;
 constexpr int kConvWarp = 12;
 constexpr int kThreads = 512;
-constexpr int kRegsSoftmax = 184, kRegsMma = 48, kRegsConv = 96;
+constexpr int kRegsSoftmax = 192, kRegsMma = 48, kRegsConv = 80;
 static_assert(128 * (2 * kRegsSoftmax + kRegsMma + kRegsConv) <= 65536, "register split");
 constexpr uint32_t kHalf = 128 * 128;  // 128 rows of 64 halves
 constexpr uint32_t kTmemCols = 512;
-constexpr float kTop = 4.f;         // weight exponent at the reference
-constexpr float kLag = 4.f;         // the reference moves when passed by more
-constexpr float kSpread = 4.f;      // value exponents this far below the largest: float32 sums
+constexpr float kTop = 7.f;         // weight exponent at the reference
+constexpr float kLag = 8.f;         // the reference moves when passed by more
 __host__ __device__ constexpr uint32_t col_s(int t) { return t ? 128u : 0u; }
 __host__ __device__ constexpr uint32_t col_o(int t) { return t ? 384u : 256u; }
 
 struct Bars {
-  uint64_t k_full[kStagesK];   // K tile expanded (one arrival per converter warp)
-  uint64_t v_full[kStagesV];
-  uint64_t k_empty[kStagesK];  // last Q.K of the stage done
-  uint64_t v_empty[kStagesV];  // last P.V of the stage done
+  uint64_t raw_full[2];        // the K, V codes of a tile landed
+  uint64_t raw_empty[2];       // they are in the converters' registers
+  uint64_t k_full[kStages];    // K tile expanded (one arrival per converter warp)
+  uint64_t v_full[kStages];
+  uint64_t k_empty[kStages];  // last Q.K of the stage done
+  uint64_t v_empty[kStages];  // last P.V of the stage done
   uint64_t s_full[2], p_full[2], o_done[2], drain[2];
+  uint64_t turn[2][4];         // warp w of softmax t has made its weights of a tile
   uint32_t tmem_base, abort;
   int32_t row, pair;
-  // factor 2^ek and exponent ev of the blocks of recent KV tiles: the slot of
-  // tile j is rewritten for tile j + 8, which is expanded only after Q.K(j +
-  // 5), and that only after the softmax of tile j + 4
-  float ks[kScaleSlots][kPages];
-  float ev[kScaleSlots][kPages];
+  // what the CTA works on; the roles read it where they need it (kept in
+  // registers from the prologue on, it would spill)
+  int32_t seq_len, n_tiles, npages, lo_pg, first_pos, last_pos, table_row;
+  // Of each block of recent KV tiles: 2^ek, ev, 2^-ev.  The slot of tile j is rewritten for tile j +
+  // 4, which is expanded only after Q.K(j + 2) of both query tiles, and that
+  // is queued only after their softmax of tile j + 1.
+  alignas(16) float scales[kScaleSlots][kPages][4];
   int32_t nan_first[128], nan_last[128];  // by dim: keys whose value is NaN
 };
 
@@ -105,15 +115,18 @@ struct Smem {
   static constexpr uint32_t kTile = kBM * D * 2;  // Q, K or V tile of halves
   static constexpr uint32_t q = 0;                // Q0 | Q1 (float32: high | low)
   static constexpr uint32_t k = q + 2 * kTile;
-  static constexpr uint32_t v = k + kStagesK * kTile;
-  static constexpr uint32_t bars = v + kStagesV * kTile;
+  static constexpr uint32_t v = k + kStages * kTile;
+  static constexpr uint32_t raw = v + kStages * kTile;    // K codes | V codes
+  static constexpr uint32_t kRaw = kBN * D;
+  static constexpr uint32_t bars = raw + 2 * kRaw;
   static constexpr uint32_t total = bars + sizeof(Bars) + 1024;  // + alignment of the base
 };
+static_assert(kScaleSlots > kStages + 1, "a slot outlives its softmax");
 static_assert(Smem<128>::total <= 227 * 1024, "shared memory");
 
 struct Params {
-  const uint8_t* k_cache;
-  const uint8_t* v_cache;
+  CUtensorMap tmap_k;  // [num_blocks * Hkv * 16 rows][D] bytes, box 16 rows x D
+  CUtensorMap tmap_v;
   const uint8_t* k_scales;
   const uint8_t* v_scales;
   int64_t scale_stride;
@@ -128,7 +141,7 @@ struct Params {
   int32_t window;
   uint32_t* error_word;
   uint64_t wait_ns;
-  int32_t withhold_tile;      // test hook: CTA 0 never announces this K tile (-1: none)
+  int32_t withhold_tile;      // test hook: CTA 0 never copies this raw K tile (-1: none)
 };
 
 __device__ __forceinline__ void abort_cta(Bars* B, uint32_t* error_word) {
@@ -142,17 +155,6 @@ __device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, Ba
   return false;
 }
 
-// 2^x of a pair of halves; 2^-inf = 0
-__device__ __forceinline__ uint32_t ex2_f16x2(uint32_t x) {
-  uint32_t y;
-  asm("ex2.approx.f16x2 %0, %1;" : "=r"(y) : "r"(x));
-  return y;
-}
-__device__ __forceinline__ uint32_t add_f16x2(uint32_t a, uint32_t b) {
-  uint32_t y;
-  asm("add.rn.f16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
-  return y;
-}
 __device__ __forceinline__ uint32_t halves(float lo, float hi) {
   return decode::as_u32(__floats2half2_rn(lo, hi));
 }
@@ -167,11 +169,13 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
 __device__ __forceinline__ uint32_t swz(uint32_t row, uint32_t chunk) {
   return row * 128u + ((chunk ^ (row & 7u)) << 4);
 }
-__device__ __forceinline__ uint4 ld_codes(const uint8_t* p) {
-  uint4 v;
-  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
+__device__ __forceinline__ void sts128(uint32_t addr, const uint32_t (&r)[4]) {
+  asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
+               : "memory");
+}
+__device__ __forceinline__ float4 lds_float4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));
   return v;
 }
 __device__ __forceinline__ void order_after_previous_grid() {
@@ -271,13 +275,16 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
   const int lo_pg = key_lo / kPage;
   const int nt = n_tiles - j_lo;
 
+  if ((warp == 8 || warp == 9) && lane == 0) tc::prefetch_tensormap(warp == 8 ? &p.tmap_k : &p.tmap_v);
   if (threadIdx.x == 0) {
     const uint32_t issuers = has_t1 ? 2u : 1u;
-    for (int s = 0; s < kStagesK; ++s) {
+    for (int h = 0; h < 2; ++h) {
+      mbar_init(&B->raw_full[h], 1);
+      mbar_init(&B->raw_empty[h], 4);
+    }
+    for (int s = 0; s < kStages; ++s) {
       mbar_init(&B->k_full[s], 4);
       mbar_init(&B->k_empty[s], issuers);
-    }
-    for (int s = 0; s < kStagesV; ++s) {
       mbar_init(&B->v_full[s], 4);
       mbar_init(&B->v_empty[s], issuers);
     }
@@ -286,8 +293,16 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       mbar_init(&B->p_full[t], 4);
       mbar_init(&B->o_done[t], 1);
       mbar_init(&B->drain[t], 1);
+      for (int w = 0; w < 4; ++w) mbar_init(&B->turn[t][w], 1);
     }
     B->abort = 0;
+    B->seq_len = L;
+    B->n_tiles = n_tiles;
+    B->npages = npages;
+    B->lo_pg = lo_pg;
+    B->first_pos = start + tok0;
+    B->last_pos = start + last_tok;
+    B->table_row = r;
     fence_barrier_init();
   }
   if (threadIdx.x < 128) {
@@ -302,117 +317,123 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = B->tmem_base;
+  // Lane i < 8: block of page i of tile j as the table has it, or -1 where the
+  // page is not read.
+  const volatile Bars* VB = B;
+  auto reads_page = [&](int j) {
+    const int pg = j * kPages + lane;
+    return lane < kPages && j < VB->n_tiles && pg < VB->npages && pg >= VB->lo_pg;
+  };
+  auto table_ids = [&](int j) {
+    return reads_page(j) ? p.block_tables[(int64_t)VB->table_row * p.max_blocks_per_seq + j * kPages + lane] : -1;
+  };
 
   if (warp >= kConvWarp) {
     // ------------------------------------------------------------ converters
     tc::regs_dec<kRegsConv>();
     // Thread ct of 128 owns a 16-byte chunk of a page row: D = 128, one page
-    // a round; D = 64, two.
+    // a round; D = 64, two.  Of every 8 neighbouring lanes 4 have the chunks of
+    // one half of a row and 4 the same of another row (D = 128: the row XOR
+    // 5), so that they never meet in a bank: neither where they read the
+    // codes nor where they write the halves.
     constexpr int kChunks = D / 16;                // chunks of a row
     constexpr int kPerRound = 128 / (kPage * kChunks);  // pages of a round
     constexpr int kRounds = kPages / kPerRound;
     const int ct = threadIdx.x - kConvWarp * 32;
-    const int c = ct % kChunks, prow = ct / kChunks % kPage, psub = ct / (kChunks * kPage);
-    // the lane's two 16-byte stores: dims 16 c .. 16 c + 7 and the next 8; at
-    // D = 128 the upper half's lanes store theirs in the other order, so that
-    // the 8 lanes of a row never meet in a bank
-    const int first = D == 128 ? c >> 2 : 0;
-    const uint32_t hbase = (uint32_t)(c / 4) * kHalf;
-    const int ch0 = (2 * c + first) & 7, ch1 = (2 * c + 1 - first) & 7;
-    auto page_of = [&](int j, int i) { return j * kPages + i; };
-    // lane i < 8: block of page i of tile j (-1: none, read as zeros)
-    auto block_ids = [&](int j) {
-      const int pg = page_of(j, lane);
-      const bool in = lane < kPages && j < n_tiles && pg < npages && pg >= lo_pg;
-      int b = in ? __ldg(p.block_tables + (int64_t)r * W + pg) : -1;
-      if (in && (b < 0 || b >= p.num_blocks)) {
-        b = -1;
-        set_error(p.error_word, CB_DEVERR_BLOCK_RANGE);
-      }
-      return b;
+    const int even = ((ct >> 2) & 6) | ((ct >> 2) & 8);
+    const int prow = D == 128 ? ((ct & 4) ? even ^ 5 : even) : (ct >> 2) & 15;
+    const int c = D == 128 ? ((ct >> 6) << 2) | (ct & 3) : ct & 3;
+    const int psub = D == 128 ? 0 : ct >> 6;
+    // where the TMA swizzle put the chunk, and where its halves go: dims 16 c
+    // .. 16 c + 7 and the next 8 of the row (rows of a round lie 16 rows or 32
+    // after those of the last, so the swizzle is the same)
+    const uint32_t raw_at = smem_addr(smem + Smem<D>::raw) + (uint32_t)psub * (kPage * D) +
+                            (D == 128 ? prow * 128 + ((c ^ (prow & 7)) << 4) : prow * 64 + ((c ^ ((prow >> 1) & 3)) << 4));
+    const uint32_t out_at = smem_addr(smem) + (uint32_t)(c / 4) * kHalf + (uint32_t)psub * (kPage * 128);
+    const uint32_t out_a = out_at + swz(prow, (2 * c) & 7), out_b = out_at + swz(prow, (2 * c + 1) & 7);
+    auto store = [&](uint32_t tile, int i, const uint32_t (&w)[4]) {
+      uint32_t a[4], b[4];
+      q8::halves4(w[0], a[0], a[1]);
+      q8::halves4(w[1], a[2], a[3]);
+      q8::halves4(w[2], b[0], b[1]);
+      q8::halves4(w[3], b[2], b[3]);
+      const uint32_t at = tile + i * (kPerRound * kPage * 128);
+      sts128(out_a + at, a);
+      sts128(out_b + at, b);
     };
-    auto load = [&](const uint8_t* cache, int ids, uint4* raw) {
+    // raw tile h (0: K, 1: V) of ring turn jj into registers
+    auto take = [&](int h, int jj, uint32_t (&w)[kRounds][4]) {
+      if (!__all_sync(0xffffffffu, mbar_wait(&B->raw_full[h], jj & 1, p.wait_ns))) return false;
 #pragma unroll
-      for (int i = 0; i < kRounds; ++i) {
-        const int b = __shfl_sync(0xffffffffu, ids, i * kPerRound + psub);
-        raw[i] = b >= 0 ? ld_codes(cache + ((int64_t)b * Hkv + g) * (kPage * D) + prow * D + c * 16)
-                        : make_uint4(0, 0, 0, 0);
-      }
+      for (int i = 0; i < kRounds; ++i) decode::lds128(raw_at + h * Smem<D>::kRaw + i * (kPerRound * kPage * D), w[i]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&B->raw_empty[h]);
+      return true;
     };
-    auto store = [&](uint8_t* tile, int i, uint4 w) {
-      const uint32_t row = (uint32_t)((i * kPerRound + psub) * kPage + prow);
-      uint4 a, b;
-      q8::halves4(w.x, a.x, a.y);
-      q8::halves4(w.y, a.z, a.w);
-      q8::halves4(w.z, b.x, b.y);
-      q8::halves4(w.w, b.z, b.w);
-      uint8_t* base = tile + hbase;
-      *reinterpret_cast<uint4*>(base + swz(row, ch0)) = first ? b : a;
-      *reinterpret_cast<uint4*>(base + swz(row, ch1)) = first ? a : b;
+    // Scale bytes of a tile (requested one tile ahead): lane i < 8 page i's K,
+    // lane 8 + i its V; 1 for a page that is not read.
+    auto scale_bytes = [&](int ids) {
+      const int b = __shfl_sync(0xffffffffu, ids, lane & 7);
+      uint32_t v = 127;
+      if (lane < 2 * kPages && b >= 0 && b < p.num_blocks)
+        v = (lane < kPages ? p.k_scales : p.v_scales)[(int64_t)b * p.scale_stride + g];
+      return v;
     };
-    uint4 kr[kRounds], vr[kRounds];
-    int ids = block_ids(j_lo);
-    load(p.k_cache, ids, kr);
-    load(p.v_cache, ids, vr);
+    uint32_t bytes = 127;
+    int ids_next = -1;
+    if (warp == kConvWarp) {
+      bytes = scale_bytes(table_ids(j_lo));
+      ids_next = table_ids(j_lo + 1);
+    }
     bool ok = true;
+    uint32_t w[kRounds][4];
     for (int jj = 0; jj < nt && ok; ++jj) {
       const int j = j_lo + jj;
-      const int next = block_ids(j + 1);
-      // scales of this tile: lane i < 8 its K scale, lane 8 + i its V scale
-      int e = 0;
-      {
-        // (a block that is not read takes the first one's that is, so that it
-        // does not widen the tile's range of exponents)
-        const uint32_t read = __ballot_sync(0xffffffffu, ids >= 0) & 0xffu;
-        const int own = __shfl_sync(0xffffffffu, ids, lane & 7);
-        const int any = __shfl_sync(0xffffffffu, ids, read ? __ffs(read) - 1 : 0);
-        const int b = own >= 0 ? own : any;
-        if (warp == kConvWarp && lane < 2 * kPages && b >= 0)
-          e = q8::exp_of((lane < kPages ? p.k_scales : p.v_scales)[(int64_t)b * p.scale_stride + g]);
-      }
       // ---- K
-      const int sk = jj % kStagesK;
-      if (jj >= kStagesK) {
-        ok = __all_sync(0xffffffffu, mbar_wait(&B->k_empty[sk], ((jj / kStagesK) - 1) & 1, p.wait_ns));
-        if (!ok) { abort_cta(B, p.error_word); break; }
-      }
+      const int st = jj % kStages;
+      ok = take(0, jj, w);
+      if (ok && jj >= kStages)
+        ok = __all_sync(0xffffffffu, mbar_wait(&B->k_empty[st], ((jj / kStages) - 1) & 1, p.wait_ns));
+      if (!ok) { abort_cta(B, p.error_word); break; }
       if (*reinterpret_cast<volatile uint32_t*>(&B->abort)) break;
-      uint8_t* kt = smem + Smem<D>::k + sk * kTile;
+      const uint32_t kt = Smem<D>::k + st * kTile;
 #pragma unroll
-      for (int i = 0; i < kRounds; ++i) store(kt, i, kr[i]);
-      if (warp == kConvWarp && lane < 2 * kPages) {
-        if (lane < kPages) B->ks[jj % kScaleSlots][lane] = q8::exp2i(e);
-        else B->ev[jj % kScaleSlots][lane - kPages] = (float)e;
+      for (int i = 0; i < kRounds; ++i) store(kt, i, w[i]);
+      if (warp == kConvWarp) {
+        const int e = q8::exp_of(bytes);
+        const int ev = __shfl_sync(0xffffffffu, e, kPages + (lane & 7));
+        if (lane < kPages)
+          *reinterpret_cast<float4*>(B->scales[jj % kScaleSlots][lane]) =
+              make_float4(q8::exp2i(e), (float)ev, q8::exp2i(-ev), 0.f);
       }
       fence_proxy_async_smem();
       __syncwarp();
-      // test hook: the withheld tile is never announced, so the bounded waits
-      // on it run out
-      if (lane == 0 && !(blockIdx.x == 0 && jj == p.withhold_tile)) mbar_arrive(&B->k_full[sk]);
-      load(p.k_cache, next, kr);                   // in flight while V is expanded
-      // ---- V
-      const int sv = jj % kStagesV;
-      if (jj >= kStagesV) {
-        ok = __all_sync(0xffffffffu, mbar_wait(&B->v_empty[sv], ((jj / kStagesV) - 1) & 1, p.wait_ns));
-        if (!ok) { abort_cta(B, p.error_word); break; }
+      if (lane == 0) mbar_arrive(&B->k_full[st]);
+      if (warp == kConvWarp) {
+        bytes = scale_bytes(ids_next);
+        ids_next = table_ids(j + 2);
       }
-      uint8_t* vt = smem + Smem<D>::v + sv * kTile;
+      // ---- V
+      ok = take(1, jj, w);
+      if (ok && jj >= kStages)
+        ok = __all_sync(0xffffffffu, mbar_wait(&B->v_empty[st], ((jj / kStages) - 1) & 1, p.wait_ns));
+      if (!ok) { abort_cta(B, p.error_word); break; }
+      const uint32_t vt = Smem<D>::v + st * kTile;
       const int kbase = j * kBN;
-      const int end = L - kbase;                   // rows past the sequence become zeros
+      const int end = VB->seq_len - kbase;         // rows past the sequence become zeros
       // some row of the CTA does not see all keys of this tile
-      const bool part = kbase + kBN - 1 > start + tok0 ||
-                        (p.window > 0 && kbase < start + last_tok - p.window + 1);
+      const bool part = kbase + kBN - 1 > VB->first_pos || (p.window > 0 && kbase < VB->last_pos - p.window + 1);
       if (!part) {
 #pragma unroll
-        for (int i = 0; i < kRounds; ++i) store(vt, i, vr[i]);
+        for (int i = 0; i < kRounds; ++i) store(vt, i, w[i]);
       } else {
 #pragma unroll
         for (int i = 0; i < kRounds; ++i) {
           const int row = (i * kPerRound + psub) * kPage + prow;
-          uint4 w = vr[i];
-          if (row >= end) w = make_uint4(0, 0, 0, 0);
-          if (nan_codes(w.x) | nan_codes(w.y) | nan_codes(w.z) | nan_codes(w.w)) {
-            uint32_t x[4] = {w.x, w.y, w.z, w.w};
+          uint32_t x[4];
+#pragma unroll
+          for (int b = 0; b < 4; ++b) x[b] = row < end ? w[i][b] : 0u;
+          if (nan_codes(x[0]) | nan_codes(x[1]) | nan_codes(x[2]) | nan_codes(x[3])) {
 #pragma unroll
             for (int b = 0; b < 16; ++b)
               if (((x[b >> 2] >> (8 * (b & 3))) & 0x7fu) == 0x7fu) {
@@ -420,21 +441,58 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                 atomicMin(&B->nan_first[16 * c + b], kbase + row);
                 atomicMax(&B->nan_last[16 * c + b], kbase + row);
               }
-            w = make_uint4(x[0], x[1], x[2], x[3]);
           }
-          store(vt, i, w);
+          store(vt, i, x);
         }
       }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&B->v_full[sv]);
-      load(p.v_cache, next, vr);
-      ids = next;
+      if (lane == 0) mbar_arrive(&B->v_full[st]);
     }
   } else if (warp >= 8) {
-    // ------------------------------------------------------------------ MMA
     tc::regs_dec<kRegsMma>();
-    if (warp >= kMmaWarp) {
+    if (warp < kMmaWarp) {
+      // ---------------------------------------------------------- producers
+      // Lane i (0..7) looks up page i of a tile (the next tile's ids are
+      // requested before the current tile's copies are issued); lane 0 issues
+      // the boxes.  A page that is not read uses a row past the end of the
+      // tensor map, which the TMA engine reads as zeros.
+      const int h = warp - 8;
+      const CUtensorMap* tmap = h ? &p.tmap_v : &p.tmap_k;
+      const int oob_row = p.num_blocks * Hkv * kPage;
+      uint8_t* raw = smem + Smem<D>::raw + h * Smem<D>::kRaw;
+      int next = table_ids(j_lo);
+      int issued = 0;
+      for (int jj = 0; jj < nt; ++jj) {
+        int row = oob_row;
+        if (reads_page(j_lo + jj)) {
+          if (next >= 0 && next < p.num_blocks)
+            row = (next * Hkv + g) * kPage;
+          else if (h == 0)
+            set_error(p.error_word, CB_DEVERR_BLOCK_RANGE);
+        }
+        next = table_ids(j_lo + jj + 1);
+        if (jj >= 1) {
+          const bool ok = __all_sync(0xffffffffu, mbar_wait(&B->raw_empty[h], (jj - 1) & 1, p.wait_ns));
+          if (!ok) { abort_cta(B, p.error_word); break; }
+        }
+        if (*reinterpret_cast<volatile uint32_t*>(&B->abort)) break;
+        if (lane == 0) mbar_arrive_expect_tx(&B->raw_full[h], Smem<D>::kRaw);
+        // test hook: the withheld tile is announced but never copied, so the
+        // bounded waits on it run out
+        const bool withhold = h == 0 && blockIdx.x == 0 && jj == p.withhold_tile;
+#pragma unroll
+        for (int i = 0; i < kPages; ++i) {
+          const int rr = __shfl_sync(0xffffffffu, row, i);
+          if (lane == 0 && !withhold) tc::tma_load_2d(raw + i * (kPage * D), tmap, 0, rr, &B->raw_full[h]);
+        }
+        __syncwarp();
+        issued = jj + 1;
+      }
+      // drain: every issued copy lands before the CTA may exit
+      if (issued > 0) mbar_wait(&B->raw_full[h], (issued - 1) & 1, p.wait_ns);
+    } else {
+      // -------------------------------------------------------------- MMA
       asm volatile("bar.sync 1, 320;" ::: "memory");  // Q is in shared memory
       tc::fence_after_sync();
       const int t = warp - kMmaWarp;
@@ -448,9 +506,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         bool ok = true;
         for (int jj = 0; jj <= nt && ok; ++jj) {
           if (jj >= 1) {
-            const int jr = jj - 1, sp = jr % kStagesV;
+            const int jr = jj - 1, sp = jr % kStages;
             ok = wait_or_abort(&B->p_full[t], jr & 1, B, p.error_word, p.wait_ns) &&
-                 wait_or_abort(&B->v_full[sp], (jr / kStagesV) & 1, B, p.error_word, p.wait_ns);
+                 wait_or_abort(&B->v_full[sp], (jr / kStages) & 1, B, p.error_word, p.wait_ns);
             if (!ok) break;
             tc::fence_after_sync();
             const uint64_t bv = dv0 + sp * kTileDesc;
@@ -464,8 +522,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
             if (jj == nt) tc::mma_commit(&B->o_done[t]);
           }
           if (jj < nt) {
-            const int s = jj % kStagesK;
-            ok = wait_or_abort(&B->k_full[s], (jj / kStagesK) & 1, B, p.error_word, p.wait_ns);
+            const int s = jj % kStages;
+            ok = wait_or_abort(&B->k_full[s], (jj / kStages) & 1, B, p.error_word, p.wait_ns);
             if (!ok) break;
             tc::fence_after_sync();
             const uint64_t bk = dk0 + s * kTileDesc;
@@ -552,16 +610,15 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     const bool active = t == 0 || has_t1;
     const uint32_t trow = tmem + ((uint32_t)((warp & 3) * 32) << 16);
     const uint32_t colS = col_s(t), colO = col_o(t);
-    float m_run = -INFINITY, l_run = 0.f, e_run = -INFINITY;
+    float m_run = -INFINITY, l_run = 0.f;
     bool ok = active;
     // keys before key_row are outside this row's window
     const int key_row = p.window > 0 ? pos - p.window + 1 : -(1 << 30);
     for (int jj = 0; jj < nt && ok; ++jj) {
-      // the two warpgroups take turns, so that each runs alone on the SM's
-      // exponential and FMA units while the tensor core works for the other
+      // Warps w and 4 + w, which share a quarter of the SM, take turns on its
+      // exponential and FMA units while the tensor core works for the other.
       if (has_t1 && (t == 1 || jj >= 1)) {
-        const bool tw = __all_sync(0xffffffffu, t == 0 ? mbar_wait(&B->p_full[1], (jj - 1) & 1, p.wait_ns)
-                                                     : mbar_wait(&B->p_full[0], jj & 1, p.wait_ns));
+        const bool tw = __all_sync(0xffffffffu, mbar_wait(&B->turn[t ^ 1][warp & 3], (t == 0 ? jj - 1 : jj) & 1, p.wait_ns));
         if (!tw) { abort_cta(B, p.error_word); ok = false; break; }
       }
       // S(j) ready implies that the tile's scales are in shared memory: they
@@ -580,14 +637,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
 #pragma unroll
         for (int i = 0; i < kBN; ++i) sv[i] = (i <= lim && i >= lo) ? sv[i] : -INFINITY;
       }
-      float f[kPages], ev[kPages];
-#pragma unroll
-      for (int b = 0; b < kPages; b += 4) {
-        const float4 x = *reinterpret_cast<const float4*>(&B->ks[jj % kScaleSlots][b]);
-        const float4 y = *reinterpret_cast<const float4*>(&B->ev[jj % kScaleSlots][b]);
-        f[b] = x.x * hs; f[b + 1] = x.y * hs; f[b + 2] = x.z * hs; f[b + 3] = x.w * hs;
-        ev[b] = y.x; ev[b + 1] = y.y; ev[b + 2] = y.z; ev[b + 3] = y.w;
-      }
+      // scales of block b of the tile (read where they are used: the scores
+      // take most of the registers)
+      const uint32_t sc = smem_addr(B->scales[jj % kScaleSlots]);
       // the row's largest x + ev: each block's largest score, scaled
       float top = -INFINITY;
 #pragma unroll
@@ -598,7 +650,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
           const float* s = sv + 16 * (b + u);
           const float a = fmax3(fmax3(s[0], s[1], s[2]), fmax3(s[3], s[4], s[5]), fmax3(s[6], s[7], s[8]));
           const float c = fmax3(fmax3(s[9], s[10], s[11]), fmax3(s[12], s[13], s[14]), s[15]);
-          z2[u] = fmaf(fmaxf(a, c), f[b + u], ev[b + u]);
+          const float4 k = lds_float4(sc + 16 * (b + u));
+          z2[u] = fmaf(fmaxf(a, c), k.x * hs, k.y);
         }
         top = fmax3(top, z2[0], z2[1]);
       }
@@ -609,26 +662,24 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       // a row with every key so far masked has m = -inf: subtract 0 instead,
       // so that its masked scores give 2^-inf = 0 rather than NaN
       const float m_sub = m_run == -INFINITY ? 0.f : m_run;
-      const float e_max = fmax3(fmax3(ev[0], ev[1], ev[2]), fmax3(ev[3], ev[4], ev[5]), fmaxf(ev[6], ev[7]));
-      const float e_min = -fmax3(fmax3(-ev[0], -ev[1], -ev[2]), fmax3(-ev[3], -ev[4], -ev[5]), fmaxf(-ev[6], -ev[7]));
-      e_run = fmaxf(e_run, e_max);
       float lsum = 0.f;
       if constexpr (kF32) {
 #pragma unroll
         for (int b = 0; b < kPages; ++b) {
-          const float base = ev[b] - m_sub;
+          const float4 k = lds_float4(sc + 16 * b);
+          const float f = k.x * hs, base = k.y - m_sub;
           float bs = 0.f;
           uint32_t hi[8], lw[8];
 #pragma unroll
           for (int i = 0; i < 16; i += 2) {
-            const float p0 = ex2_approx(fmaf(sv[16 * b + i], f[b], base));
-            const float p1 = ex2_approx(fmaf(sv[16 * b + i + 1], f[b], base));
+            const float p0 = ex2_approx(fmaf(sv[16 * b + i], f, base));
+            const float p1 = ex2_approx(fmaf(sv[16 * b + i + 1], f, base));
             bs += p0 + p1;
             hi[i / 2] = halves(p0, p1);
             const float2 h = floats(hi[i / 2]);
             lw[i / 2] = halves(p0 - h.x, p1 - h.y);
           }
-          lsum = fmaf(bs, q8::exp2i(-(int)ev[b]), lsum);
+          lsum = fmaf(bs, k.z, lsum);
           // (kept in the scores' registers until all are read)
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
@@ -647,41 +698,28 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
           tc::tmem_st16(trow + colS + 64 + 8 * b, pk);
         }
       } else {
-        const bool wide = e_run - e_min > kSpread;
-        if (wide) {
-          // float32 exponentials for the sum (see the header)
-#pragma unroll
-          for (int b = 0; b < kPages; ++b) {
-            const float base = ev[b] - m_sub;
-            float bs = 0.f;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) bs += ex2_approx(fmaf(sv[16 * b + i], f[b], base));
-            lsum = fmaf(bs, q8::exp2i(-(int)ev[b]), lsum);
-          }
-        }
 #pragma unroll
         for (int h = 0; h < 4; ++h) {
           uint32_t pk[16];
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
             const int b = 2 * h + u;
-            const float base = ev[b] - m_sub;
-            const float2 f2 = make_float2(f[b], f[b]), b2 = make_float2(base, base);
+            const float4 k = lds_float4(sc + 16 * b);
+            const float f = k.x * hs, base = k.y - m_sub;
+            const float2 f2 = make_float2(f, f), b2 = make_float2(base, base);
+            float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
             for (int i = 0; i < 16; i += 2) {
-              const float2 z = __ffma2_rn(make_float2(sv[16 * b + i], sv[16 * b + i + 1]), f2, b2);
-              pk[8 * u + i / 2] = ex2_f16x2(halves(z.x, z.y));
+              float2 z = __ffma2_rn(make_float2(sv[16 * b + i], sv[16 * b + i + 1]), f2, b2);
+              z.x = ex2_approx(z.x);
+              z.y = ex2_approx(z.y);
+              sum[i / 2 & 1] = __fadd2_rn(sum[i / 2 & 1], z);
+              pk[8 * u + i / 2] = halves(z.x, z.y);
             }
-            if (!wide) {
-              // the block's sum in halves (16 weights of at most 2^8)
-              const uint32_t* q = pk + 8 * u;
-              const uint32_t s4 = add_f16x2(add_f16x2(add_f16x2(q[0], q[1]), add_f16x2(q[2], q[3])),
-                                            add_f16x2(add_f16x2(q[4], q[5]), add_f16x2(q[6], q[7])));
-              const float2 s2 = floats(s4);
-              lsum = fmaf(s2.x + s2.y, q8::exp2i(-(int)ev[b]), lsum);
-            }
+            lsum = fmaf((sum[0].x + sum[1].x) + (sum[0].y + sum[1].y), k.z, lsum);
           }
           tc::tmem_st16(trow + colS + 16 * h, pk);
+          if (h == 3 && lane == 0) mbar_arrive(&B->turn[t][warp & 3]);
         }
       }
       l_run = fmaf(l_run, alpha, lsum);
@@ -750,9 +788,13 @@ cb_status launch_kernel(const cb_attention_args& a, const uint8_t* k_scales, con
   const int64_t n = ctas(a);
   if (n <= 0) return CB_OK;
   if (n >= ((int64_t)1 << 31)) return CB_ERR_UNSUPPORTED;
+  const int64_t rows = (int64_t)a.num_blocks * a.num_kv_heads * kPage;
+  if (rows >= ((int64_t)1 << 31) - kPage) return CB_ERR_UNSUPPORTED;
   Params p{};
-  p.k_cache = static_cast<const uint8_t*>(a.k_cache);
-  p.v_cache = static_cast<const uint8_t*>(a.v_cache);
+  st = cached_cache_map(&p.tmap_k, a.k_cache, rows, D, 1);
+  if (st != CB_OK) return st;
+  st = cached_cache_map(&p.tmap_v, a.v_cache, rows, D, 1);
+  if (st != CB_OK) return st;
   p.k_scales = k_scales;
   p.v_scales = v_scales;
   p.scale_stride = scale_stride;
