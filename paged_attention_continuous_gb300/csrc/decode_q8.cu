@@ -49,7 +49,9 @@ cb_status launch(const cb_attention_args& a, const uint8_t* k_scales, const uint
   p.group = a.num_q_heads / a.num_kv_heads;
   p.parts = parts;
   p.part_heads = part_heads;
-  p.scale_log2 = a.scale * 1.4426950408889634f;
+  const double scale_log2 = (double)a.scale * 1.4426950408889634;
+  p.scale_log2 = (float)scale_log2;
+  p.scale_log2_low = p.scale_log2 != 0.f ? (float)((scale_log2 - p.scale_log2) / p.scale_log2) : 0.f;
   p.window = a.sliding_window;
   p.error_word = error_word;
   p.work_counter = s.work_counter;

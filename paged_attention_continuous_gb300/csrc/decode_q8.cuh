@@ -30,12 +30,14 @@
 //   * Queries are scaled by a power of two to the halves' range for each
 //     head, so that bfloat16 queries are halves exactly (elements under
 //     2^-29 of the head's largest lose bits); float32 queries are split into
-//     two halves (22 bits), and their weights too.
+//     two halves (22 bits), and their weights too.  With those, score
+//     exponents are rounded at their size next to the reference: scale *
+//     log2(e) is a pair of floats, the reference a whole number.
 //   * Scales never touch the codes.  With x = score * log2(e), the weight
 //     that multiplies a value code is 2^(x + ev - m): the running reference m
 //     is over x + ev, so a block of large values and a block of small ones
 //     share it, weights stay in a half's range (2^7 at the reference, 2^15
-//     at most, 2^-24 at least), and the sum of weights adds 2^(x - m) = 2^(x
+//     at most, rounded to multiples of 2^-24 at least), and the sum of weights adds 2^(x - m) = 2^(x
 //     + ev - m) * 2^-ev in float32.  Exponents lie in [-40, 40], so that no
 //     page's part of the sum can leave float32's range.
 #pragma once
@@ -62,7 +64,12 @@ using namespace decode;
 constexpr int kWarps = 8;
 constexpr int kMaxHeads = 16;  // query heads of an item
 constexpr int kPair = 2;       // pages of a stage
-constexpr float kTop = 7.f;    // weight exponent at the reference
+// weight exponent at the reference, which moves when passed by more than the
+// lag (float32: exponents near 0 are the most exact)
+template <typename T> constexpr float kTop = 7.f;
+template <> constexpr float kTop<float> = 0.f;
+template <typename T> constexpr float kLag = 8.f;
+template <> constexpr float kLag<float> = 2.f;
 
 struct Params {
   CUtensorMap tmap_k;  // [num_blocks * Hkv * 16 rows][D] bytes, box 16 rows x D
@@ -82,6 +89,7 @@ struct Params {
   int32_t parts;           // items that serve a KV head
   int32_t part_heads;      // query heads of an item (the last part may have fewer)
   float scale_log2;
+  float scale_log2_low;    // what float32 leaves of it, as a share of it
   int32_t window;
   uint32_t* error_word;
   uint32_t* work_counter;  // zero between launches
@@ -629,11 +637,12 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_kernel(const __grid_con
         float z[kPair][4];
 #pragma unroll
         for (int k = 0; k < kPair; ++k) {
-          const float f0 = hs[nt][0] * ks[k], f1 = hs[nt][1] * ks[k];
-          z[k][0] = fmaf(s[k][nt][0][0] + s[k][nt][1][0], f0, ev[k]);
-          z[k][1] = fmaf(s[k][nt][0][1] + s[k][nt][1][1], f1, ev[k]);
-          z[k][2] = fmaf(s[k][nt][0][2] + s[k][nt][1][2], f0, ev[k]);
-          z[k][3] = fmaf(s[k][nt][0][3] + s[k][nt][1][3], f1, ev[k]);
+          const float f[2] = {hs[nt][0] * ks[k], hs[nt][1] * ks[k]};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            s[k][nt][0][e] += s[k][nt][1][e];
+            z[k][e] = fmaf(s[k][nt][0][e], f[e & 1], ev[k]);
+          }
         }
         if (!whole) {
 #pragma unroll
@@ -654,11 +663,11 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_kernel(const __grid_con
           pm[0] = fmaxf(pm[0], __shfl_xor_sync(0xffffffffu, pm[0], o));
           pm[1] = fmaxf(pm[1], __shfl_xor_sync(0xffffffffu, pm[1], o));
         }
-        // the reference moves only when a step passes it by more than 2^8
+        // the reference moves only when a step passes it by more than the lag
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          const float top = pm[c] - kTop;
-          const bool up = top - m_run[nt][c] > 8.f;
+          const float top = kP == 2 ? rintf(pm[c] - kTop<T>) : pm[c] - kTop<T>;
+          const bool up = top - m_run[nt][c] > kLag<T>;
           alpha[nt][c] = up ? ex2_approx(m_run[nt][c] - top) : 1.f;
           m_run[nt][c] = up ? top : m_run[nt][c];
           resc |= up;
@@ -668,7 +677,16 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_kernel(const __grid_con
         for (int k = 0; k < kPair; ++k) {
           float w[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) w[e] = ex2_approx(z[k][e] - m_run[nt][e & 1]);
+          for (int e = 0; e < 4; ++e) {
+            float x = z[k][e] - m_run[nt][e & 1];
+            if constexpr (kP == 2) {
+              // not through z, whose rounding is that of a large exponent
+              const float f = hs[nt][e & 1] * ks[k], y = s[k][nt][0][e];
+              const float fine = fmaf(y, f * p.scale_log2_low, fmaf(y, f, ev[k] - m_run[nt][e & 1]));
+              x = z[k][e] == -INFINITY ? -INFINITY : fine;
+            }
+            w[e] = ex2_approx(x);
+          }
           sum[0] = fmaf(w[0] + w[2], inv_vs[k], sum[0]);
           sum[1] = fmaf(w[1] + w[3], inv_vs[k], sum[1]);
           // weights rounded to halves (the matrix operand), transposed to

@@ -35,7 +35,12 @@
 //     halves or bfloat16s, so the packed forms only lose bits.
 //   * float32 queries: Q and the weights are split into two halves each (22
 //     bits), one query tile per CTA (the second tile's place holds the low
-//     halves).
+//     halves).  Score exponents are rounded once: scale * log2(e) is a pair
+//     of floats, the reference a whole number near the largest exponent.  The
+//     tensor core drops bits wherever it adds to a large accumulator, so each
+//     tile's P.V starts from zero and the softmax warps add it to the output
+//     (at 1000 keys the error is that of float32 torch then, and 2 to 3
+//     times that with one accumulator).
 //   * A value code that is NaN must not reach rows that do not see its key
 //     (weight 0 times NaN is NaN): in tiles that some row of the CTA sees only
 //     in part, converters store such codes as 0 and note the first and last
@@ -84,8 +89,12 @@ constexpr int kRegsSoftmax = 192, kRegsMma = 48, kRegsConv = 80;
 static_assert(128 * (2 * kRegsSoftmax + kRegsMma + kRegsConv) <= 65536, "register split");
 constexpr uint32_t kHalf = 128 * 128;  // 128 rows of 64 halves
 constexpr uint32_t kTmemCols = 512;
-constexpr float kTop = 7.f;         // weight exponent at the reference
-constexpr float kLag = 8.f;         // the reference moves when passed by more
+// weight exponent at the reference, which moves when passed by more than the
+// lag (float32: exponents near 0 are the most exact)
+template <typename T> constexpr float kTop = 7.f;
+template <> constexpr float kTop<float> = 0.f;
+template <typename T> constexpr float kLag = 8.f;
+template <> constexpr float kLag<float> = 2.f;
 __host__ __device__ constexpr uint32_t col_s(int t) { return t ? 128u : 0u; }
 __host__ __device__ constexpr uint32_t col_o(int t) { return t ? 384u : 256u; }
 
@@ -138,6 +147,7 @@ struct Params {
   int32_t row_begin, num_rows, num_tokens;
   int32_t num_blocks, max_blocks_per_seq, num_q_heads, num_kv_heads, group;
   float scale_log2;
+  float scale_log2_low;       // what float32 leaves of it, as a share of it
   int32_t window;
   uint32_t* error_word;
   uint64_t wait_ns;
@@ -177,6 +187,11 @@ __device__ __forceinline__ float4 lds_float4(uint32_t addr) {
   float4 v;
   asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr));
   return v;
+}
+// s (f + fl) + base, rounded at the size of the result and not of s f; -inf
+// stays -inf (whatever the sign of fl)
+__device__ __forceinline__ float exponent(float s, float f, float fl, float base) {
+  return fmaf(fmaxf(s, -4294967296.f), fl, fmaf(s, f, base));
 }
 __device__ __forceinline__ void order_after_previous_grid() {
   if (blockIdx.x == 0 && threadIdx.x == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -517,7 +532,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
 #pragma unroll
               for (int kk = 0; kk < kBN / 16; ++kk)
                 tc::mma_f16_ts(tmem + col_o(t), tmem + col_s(t) + piece * 64 + kk * 8, bv + (kk * 2048 >> 4),
-                               idesc_pv, (jr > 0 || kk > 0 || piece > 0) ? 1u : 0u);
+                               idesc_pv, ((!kF32 && jr > 0) || kk > 0 || piece > 0) ? 1u : 0u);
             tc::mma_commit(&B->v_empty[sp]);
             if (jj == nt) tc::mma_commit(&B->o_done[t]);
           }
@@ -579,7 +594,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       // zeros, or a row that is not finite (nor are its scores): factor 1
       const int k = amax > 0.f && amax <= 3.402823466e38f ? max((int)(__float_as_uint(amax) >> 23) - 127, -110) : 14;
       const float up = p.scale_log2 == 0.f ? 0.f : p.scale_log2 < 0.f ? -q8::exp2i(14 - k) : q8::exp2i(14 - k);
-      hs = p.scale_log2 == 0.f ? 1.f : fabsf(p.scale_log2) * q8::exp2i(k - 14);
+      // (never so small that times a block's scale it is 0: a masked score is -inf)
+      hs = p.scale_log2 == 0.f ? 1.f : fmaxf(fabsf(p.scale_log2) * q8::exp2i(k - 14), q8::exp2i(-80));
       uint8_t* qs = smem + Smem<D>::q + t * kTile;
 #pragma unroll 4
       for (int i = 0; i < D / 8; ++i) {
@@ -655,8 +671,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         }
         top = fmax3(top, z2[0], z2[1]);
       }
-      top -= kTop;
-      const bool resc = top - m_run > kLag;       // also on a row's first visible key
+      top -= kTop<T>;
+      if constexpr (kF32) top = rintf(top);
+      const bool resc = top - m_run > kLag<T>;    // also on a row's first visible key
       const float alpha = resc ? ex2_approx(m_run - top) : 1.f;
       m_run = resc ? top : m_run;
       // a row with every key so far masked has m = -inf: subtract 0 instead,
@@ -667,13 +684,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
 #pragma unroll
         for (int b = 0; b < kPages; ++b) {
           const float4 k = lds_float4(sc + 16 * b);
-          const float f = k.x * hs, base = k.y - m_sub;
+          const float f = k.x * hs, fl = f * p.scale_log2_low, base = k.y - m_sub;
           float bs = 0.f;
           uint32_t hi[8], lw[8];
 #pragma unroll
           for (int i = 0; i < 16; i += 2) {
-            const float p0 = ex2_approx(fmaf(sv[16 * b + i], f, base));
-            const float p1 = ex2_approx(fmaf(sv[16 * b + i + 1], f, base));
+            const float p0 = ex2_approx(exponent(sv[16 * b + i], f, fl, base));
+            const float p1 = ex2_approx(exponent(sv[16 * b + i + 1], f, fl, base));
             bs += p0 + p1;
             hi[i / 2] = halves(p0, p1);
             const float2 h = floats(hi[i / 2]);
@@ -725,7 +742,19 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       l_run = fmaf(l_run, alpha, lsum);
       // S_t(j) ready implies P_t.V(j-1) completed (same issuing thread, in
       // order), so O_t is stable here and may be rescaled.
-      if (jj >= 1 && __any_sync(0xffffffffu, resc)) {
+      if (kF32 && jj >= 1) {
+        // the sum of the tiles before, in the place of the second tile's O
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) {
+          float o[16], a[16];
+          tc::tmem_ld16(trow + colO + 16 * c, o);
+          if (jj > 1) tc::tmem_ld16(trow + col_o(1) + 16 * c, a);
+          tc::tmem_wait_ld();
+#pragma unroll
+          for (int e = 0; e < 16; ++e) o[e] = (jj > 1 ? a[e] + o[e] : o[e]) * alpha;
+          tc::tmem_st16(trow + col_o(1) + 16 * c, reinterpret_cast<const uint32_t*>(o));
+        }
+      } else if (jj >= 1 && __any_sync(0xffffffffu, resc)) {
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
           float o[32];
@@ -752,6 +781,12 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         for (int c = 0; c < D / 32; ++c) {
           float o[32];
           tc::tmem_ld32_sync(trow + colO + 32 * c, o);
+          if (kF32 && nt > 1) {
+            float a[32];
+            tc::tmem_ld32_sync(trow + col_o(1) + 32 * c, a);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] += a[e];
+          }
           if (valid) {
 #pragma unroll
             for (int e = 0; e < 32; ++e) {
@@ -811,7 +846,9 @@ cb_status launch_kernel(const cb_attention_args& a, const uint8_t* k_scales, con
   p.num_q_heads = a.num_q_heads;
   p.num_kv_heads = a.num_kv_heads;
   p.group = a.num_q_heads / a.num_kv_heads;
-  p.scale_log2 = a.scale * 1.4426950408889634f;
+  const double scale_log2 = (double)a.scale * 1.4426950408889634;
+  p.scale_log2 = (float)scale_log2;
+  p.scale_log2_low = p.scale_log2 != 0.f ? (float)((scale_log2 - p.scale_log2) / p.scale_log2) : 0.f;
   p.window = a.sliding_window;
   p.error_word = error_word;
   p.wait_ns = wait_limit_ns();
