@@ -406,9 +406,15 @@ class Scheduler:
 
 
 # ------------------------------------------------------------------ GPU ops
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _dtype_code(t) -> int:
@@ -563,34 +569,62 @@ def paged_attention(q, k_cache, v_cache, cu_seqlens_q, seq_lens, block_tables, *
 
 
 # ------------------------------------------- the 8-bit cache and its operators
-def _need_i32(name, t, shape):
+# A decode step makes these calls with a GPU that is done in a few
+# microseconds, so a call looks at each tensor once, by its cheapest
+# properties, and words an error only after one is found.
+def _launch_on(t, stream) -> int:
+    """Device index of t, which has to be the current device (the launch goes
+    to its stream), and the stream to launch on."""
     torch = _torch()
-    _need_cuda(t)
-    if t.dtype != torch.int32 or tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must be int32 of shape {tuple(shape)}")
-
-
-def _need_one_device(first, *ts):
-    """Every tensor on the first one's device, and that one current: the
-    launch goes to the current device's stream."""
-    for t in ts:
-        if t is not None and t.device != first.device:
-            raise ValueError("tensors live on different devices")
-    if first.device.index != _torch().cuda.current_device():
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError("tensors must live on the GPU (no CPU path)")
+    if dev != torch.cuda.current_device():
         raise ValueError("the tensors' device is not the current device")
+    if stream is None:
+        return dev, torch._C._cuda_getCurrentRawStream(dev)
+    return dev, int(stream.cuda_stream)
 
 
-def _tables(cached_lens, block_tables, free_ring, free_state, block_size, error_word):
-    R = cached_lens.shape[0]
-    _need_i32("cached_lens", cached_lens, (R,))
-    _need_i32("block_tables", block_tables, (R, block_tables.shape[-1]))
-    _need_i32("free_ring", free_ring, (free_ring.shape[0],))
-    _need_i32("free_state", free_state, (2,))
-    _need_one_device(cached_lens, block_tables, free_ring, free_state, error_word)
-    return cb_tables(R, block_tables.shape[1], free_ring.shape[0], int(block_size),
-                     cached_lens.data_ptr(), block_tables.data_ptr(), free_ring.data_ptr(),
-                     free_state.data_ptr(),
-                     error_word.data_ptr() if error_word is not None else None)
+def _refuse(name, t, dev, dtype, what):
+    if not t.is_cuda:
+        raise ValueError("tensors must live on the GPU (no CPU path)")
+    if t.get_device() != dev:
+        raise ValueError("tensors live on different devices")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, not {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError("tensors must be contiguous")
+    raise ValueError(f"{name} must be {what}")
+
+
+def _i32(dev, named):
+    """Pointers of contiguous int32 tensors of given element counts."""
+    i32 = _torch().int32
+    ptrs = []
+    for name, t, n in named:
+        if t.get_device() != dev or t.dtype is not i32 or t.numel() != n or not t.is_contiguous():
+            if t.is_cuda and t.dtype is not i32:
+                raise ValueError(f"{name} must be int32")
+            _refuse(name, t, dev, i32, f"int32 of {n} elements")
+        ptrs.append(t.data_ptr())
+    return ptrs
+
+
+def _error_ptr(error_word, dev):
+    if error_word is None:
+        return None
+    if error_word.get_device() != dev or error_word.element_size() != 4 or error_word.numel() < 1:
+        raise ValueError("error_word must be a 4-byte word on the same device")
+    return error_word.data_ptr()
+
+
+def _tables(dev, cached_lens, block_tables, free_ring, free_state, block_size, error_word):
+    R, W = block_tables.shape
+    N = free_ring.numel()
+    p = _i32(dev, (("cached_lens", cached_lens, R), ("block_tables", block_tables, R * W),
+                   ("free_ring", free_ring, N), ("free_state", free_state, 2)))
+    return R, cb_tables(R, W, N, block_size, *p, _error_ptr(error_word, dev))
 
 
 def step_tables(q_lens, cached_lens, block_tables, free_ring, free_state, *, cu_seqlens_q,
@@ -601,16 +635,13 @@ def step_tables(q_lens, cached_lens, block_tables, free_ring, free_state, *, cu_
     blocks ``free_ring`` [num_blocks] with ``free_state`` = [head, count]; all
     int32, updated in place) and write the step's ``cu_seqlens_q`` [R + 1],
     ``seq_lens`` [R], ``slot_mapping`` [T] and ``positions`` [T]."""
-    t = _tables(cached_lens, block_tables, free_ring, free_state, block_size, error_word)
-    R, T = t.num_rows, slot_mapping.shape[0]
-    for name, x, n in (("q_lens", q_lens, R), ("cu_seqlens_q", cu_seqlens_q, R + 1),
-                       ("seq_lens", seq_lens, R), ("slot_mapping", slot_mapping, T),
-                       ("positions", positions, T)):
-        _need_i32(name, x, (n,))
-    _need_one_device(cached_lens, q_lens, cu_seqlens_q, seq_lens, slot_mapping, positions)
-    _check(_lib.cb_step_tables(ctypes.byref(t), q_lens.data_ptr(), T, cu_seqlens_q.data_ptr(),
-                               seq_lens.data_ptr(), slot_mapping.data_ptr(),
-                               positions.data_ptr(), _stream_ptr(stream)))
+    dev, st = _launch_on(cached_lens, stream)
+    R, t = _tables(dev, cached_lens, block_tables, free_ring, free_state, block_size, error_word)
+    T = slot_mapping.numel()
+    q, cu, seq, slots, pos = _i32(dev, (("q_lens", q_lens, R), ("cu_seqlens_q", cu_seqlens_q, R + 1),
+                                        ("seq_lens", seq_lens, R), ("slot_mapping", slot_mapping, T),
+                                        ("positions", positions, T)))
+    _check(_lib.cb_step_tables(ctypes.byref(t), q, T, cu, seq, slots, pos, st))
 
 
 def trim_tables(keep_lens, cached_lens, block_tables, free_ring, free_state, *,
@@ -618,10 +649,10 @@ def trim_tables(keep_lens, cached_lens, block_tables, free_ring, free_state, *,
     """cb_trim_tables: shorten the rows of a device state to ``keep_lens`` [R]
     tokens (negative: the row stays; 0: its request ended) and give their
     blocks back to the ring."""
-    t = _tables(cached_lens, block_tables, free_ring, free_state, block_size, error_word)
-    _need_i32("keep_lens", keep_lens, (t.num_rows,))
-    _need_one_device(cached_lens, keep_lens)
-    _check(_lib.cb_trim_tables(ctypes.byref(t), keep_lens.data_ptr(), _stream_ptr(stream)))
+    dev, st = _launch_on(cached_lens, stream)
+    R, t = _tables(dev, cached_lens, block_tables, free_ring, free_state, block_size, error_word)
+    keep, = _i32(dev, (("keep_lens", keep_lens, R),))
+    _check(_lib.cb_trim_tables(ctypes.byref(t), keep, st))
 
 
 ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
@@ -658,20 +689,24 @@ class RopePlan:
         return self.c.rot_dim
 
 
-def _rope_rows(name, x, out, T, d, dtype):
-    """Pointers and token strides of [T, H, d] rows; a token's heads lie
-    packed, tokens may be further apart."""
-    for n, t in ((name, x), (name + "_out", out)):
-        if not t.is_cuda:
-            raise ValueError("tensors must live on the GPU (no CPU path)")
-        if t.dim() != 3 or t.shape != x.shape or t.shape[0] != T or t.shape[2] != d or t.dtype != dtype:
-            raise ValueError(f"{n} must be [tokens, heads, {d}] of one type and shape")
-        if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != d) or \
-                (T > 1 and t.stride(0) < t.shape[1] * d):
-            raise ValueError(f"{n}: the heads of a token must lie packed")
-    H = x.shape[1]
-    return (x.data_ptr(), out.data_ptr(), x.stride(0) if T > 1 else H * d,
-            out.stride(0) if T > 1 else H * d, H)
+def _rope_rows(name, x, out, dev, T, d, dtype):
+    """Pointers, token strides and heads of [T, H, d] rows; a token's heads
+    lie packed, tokens may be further apart."""
+    shape = x.shape
+    if len(shape) != 3 or shape[0] != T or shape[2] != d or out.shape != shape:
+        raise ValueError(f"{name} and {name}_out must be [{T}, heads, {d}]")
+    H = shape[1]
+    strides = []
+    for t in (x, out):
+        if t.get_device() != dev:
+            raise ValueError("tensors must live on one GPU")
+        if t.dtype is not dtype:
+            raise ValueError("q, k and their outputs must be of one type")
+        s = t.stride()
+        if (d > 1 and s[2] != 1) or (H > 1 and s[1] != d) or (T > 1 and s[0] < H * d):
+            raise ValueError(f"{name}: the heads of a token must lie packed")
+        strides.append(s[0] if T > 1 else H * d)
+    return x.data_ptr(), out.data_ptr(), strides[0], strides[1], H
 
 
 def rope(q, k, positions, plan: RopePlan, *, q_out=None, k_out=None, inverse: bool = False,
@@ -684,43 +719,60 @@ def rope(q, k, positions, plan: RopePlan, *, q_out=None, k_out=None, inverse: bo
     first = q if q is not None else k
     if first is None:
         raise ValueError("neither q nor k is given")
-    T, d = first.shape[0], plan.c.head_dim
-    a = cb_rope_args()
-    a.plan, a.num_tokens, a.dtype, a.inverse = plan._p, T, _dtype_code(first), int(bool(inverse))
+    dev, st = _launch_on(first, stream)
+    T, d, dtype = first.shape[0], plan.c.head_dim, first.dtype
+    qa = ka = (None, None, 0, 0, 0)
     if q is not None:
-        q_out = torch.empty_like(q) if q_out is None else q_out
-        a.q, a.q_out, a.q_stride, a.q_out_stride, a.num_q_heads = _rope_rows("q", q, q_out, T, d, first.dtype)
+        if q_out is None:
+            q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
+        qa = _rope_rows("q", q, q_out, dev, T, d, dtype)
     if k is not None:
-        k_out = torch.empty_like(k) if k_out is None else k_out
-        a.k, a.k_out, a.k_stride, a.k_out_stride, a.num_kv_heads = _rope_rows("k", k, k_out, T, d, first.dtype)
-    _need_i32("positions", positions, (T,))
-    _need_one_device(first, k, q_out, k_out, positions)
-    a.positions = positions.data_ptr()
-    _check(_lib.cb_rope(ctypes.byref(a), _stream_ptr(stream)))
+        if k_out is None:
+            k_out = torch.empty_like(k, memory_format=torch.contiguous_format)
+        ka = _rope_rows("k", k, k_out, dev, T, d, dtype)
+    pos, = _i32(dev, (("positions", positions, T),))
+    a = cb_rope_args(plan._p, pos, T, qa[4], ka[4], _dtype_code(first), 1 if inverse else 0, *qa[:4], *ka[:4])
+    _check(_lib.cb_rope(ctypes.byref(a), st))
     return q_out, k_out
 
 
-def _need_q8(k_cache, v_cache, k_scales, v_scales):
-    """Shape (num_blocks, Hkv, block_size, D) of an 8-bit cache and the bytes
-    between two blocks' scales."""
+def _q8(dev, k_cache, v_cache, k_scales, v_scales):
+    """Shape (num_blocks, Hkv, block_size, D) of an 8-bit cache, the bytes
+    between two blocks' scales, and the four pointers."""
     torch = _torch()
-    _need_cuda(k_cache, v_cache)
-    if k_cache.dtype != torch.float8_e4m3fn or v_cache.dtype != torch.float8_e4m3fn:
-        raise TypeError("an 8-bit cache holds float8_e4m3fn codes")
-    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape:
+    codes, u8 = torch.float8_e4m3fn, torch.uint8
+    shape = k_cache.shape
+    if len(shape) != 4 or v_cache.shape != shape:
         raise ValueError("k_cache and v_cache must be [num_blocks, Hkv, block_size, D]")
-    nb, hkv, bs, d = k_cache.shape
-    for t in (k_scales, v_scales):
-        if not t.is_cuda:
-            raise ValueError("tensors must live on the GPU (no CPU path)")
-        if t.dtype != torch.uint8 or tuple(t.shape) != (nb, hkv):
-            raise ValueError("scales must be uint8 [num_blocks, Hkv]")
-    ss = max(k_scales.stride(0), hkv) if nb > 1 else hkv
-    for t in (k_scales, v_scales):
-        if (hkv > 1 and t.stride(1) != 1) or (nb > 1 and t.stride(0) != ss):
-            raise ValueError("scales: a block's must lie packed, at one stride for K and V")
-    _need_one_device(k_cache, v_cache, k_scales, v_scales)
-    return nb, hkv, bs, d, ss
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        if t.get_device() != dev or t.dtype is not codes or not t.is_contiguous():
+            _refuse(name, t, dev, codes, "contiguous")
+    nb, hkv, bs, d = shape
+    want = (nb, hkv)
+    ss = k_scales.stride()
+    if k_scales.shape != want or v_scales.shape != want:
+        raise ValueError("scales must be [num_blocks, Hkv]")
+    if v_scales.stride() != ss or (hkv > 1 and ss[1] != 1) or (nb > 1 and ss[0] < hkv):
+        raise ValueError("scales: a block's must lie packed, at one stride for K and V")
+    for name, t in (("k_scales", k_scales), ("v_scales", v_scales)):
+        if t.get_device() != dev or t.dtype is not u8:
+            if t.is_cuda and t.dtype is not u8:
+                raise ValueError("scales must be uint8")
+            _refuse(name, t, dev, u8, "[num_blocks, Hkv]")
+    return (shape, ss[0] if nb > 1 else hkv, k_cache.data_ptr(), v_cache.data_ptr(),
+            k_scales.data_ptr(), v_scales.data_ptr())
+
+
+def _rows3(name, t, dev, dtype, T, H, d):
+    """Pointer of a contiguous [T, H, d] tensor (H None: any)."""
+    s = t.shape
+    if len(s) != 3 or s[0] != T or s[2] != d or (H is not None and s[1] != H):
+        raise ValueError(f"{name} must be [{T}, {'heads' if H is None else H}, {d}]")
+    if t.get_device() != dev or not t.is_contiguous():
+        _refuse(name, t, dev, t.dtype, "contiguous")
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
+    return t.data_ptr()
 
 
 def kv_append_q8(k_new, v_new, slot_mapping, k_cache, v_cache, k_scales, v_scales, *,
@@ -731,36 +783,31 @@ def kv_append_q8(k_new, v_new, slot_mapping, k_cache, v_cache, k_scales, v_scale
     ``k_scales``/``v_scales`` uint8 [num_blocks, Hkv].  With ``rope`` (and
     ``positions`` int32 [T]) k is rotated first, and ``q`` [T, Hq, D]
     (optional) into ``q_out``, which is returned."""
-    torch = _torch()
-    _need_cuda(k_new, v_new, slot_mapping)
-    nb, hkv, bs, d, ss = _need_q8(k_cache, v_cache, k_scales, v_scales)
-    T = slot_mapping.shape[0]
-    _need_i32("slot_mapping", slot_mapping, (T,))
-    for t in (k_new, v_new):
-        if tuple(t.shape) != (T, hkv, d) or t.dtype != k_new.dtype:
-            raise ValueError(f"k_new and v_new must be [{T}, {hkv}, {d}] of one type")
-    a = cb_append_q8_args(k_new.data_ptr(), v_new.data_ptr(), slot_mapping.data_ptr(), T,
-                          _dtype_code(k_new), k_cache.data_ptr(), v_cache.data_ptr(),
-                          k_scales.data_ptr(), v_scales.data_ptr(), ss, nb, hkv, d, bs)
+    dev, st = _launch_on(k_cache, stream)
+    (nb, hkv, bs, d), ss, kc, vc, ks, vs = _q8(dev, k_cache, v_cache, k_scales, v_scales)
+    T, dtype = slot_mapping.numel(), k_new.dtype
+    slots, = _i32(dev, (("slot_mapping", slot_mapping, T),))
+    kp = _rows3("k_new", k_new, dev, dtype, T, hkv, d)
+    vp = _rows3("v_new", v_new, dev, dtype, T, hkv, d)
+    plan = pos = qp = op = None
+    hq = 0
     if rope is not None:
         if positions is None:
             raise ValueError("rope needs positions")
-        _need_i32("positions", positions, (T,))
-        a.rope, a.positions = rope._p, positions.data_ptr()
+        plan = rope._p
+        pos, = _i32(dev, (("positions", positions, T),))
+        if q is not None:
+            if q_out is None:
+                q_out = _torch().empty_like(q)
+            hq = q.shape[1]
+            qp = _rows3("q", q, dev, dtype, T, None, d)
+            op = _rows3("q_out", q_out, dev, dtype, T, hq, d)
     elif q is not None or positions is not None:
         raise ValueError("q and positions go with rope")
-    if q is not None:
-        q_out = torch.empty_like(q) if q_out is None else q_out
-        _need_cuda(q, q_out)
-        if q.dim() != 3 or q.shape[0] != T or q.shape[2] != d or q.dtype != k_new.dtype or \
-                q_out.shape != q.shape or q_out.dtype != q.dtype:
-            raise ValueError(f"q and q_out must be [{T}, Hq, {d}] of k_new's type")
-        a.q, a.q_out, a.num_q_heads = q.data_ptr(), q_out.data_ptr(), q.shape[1]
-    _need_one_device(k_cache, k_new, v_new, slot_mapping, positions, q, q_out, error_word)
-    if error_word is not None:
-        a.error_word = error_word.data_ptr()
-    _check(_lib.cb_kv_append_q8(ctypes.byref(a), _stream_ptr(stream)))
-    return q_out
+    a = cb_append_q8_args(kp, vp, slots, T, _dtype_code(k_new), kc, vc, ks, vs, ss, nb, hkv, d, bs,
+                          plan, pos, qp, op, hq, _error_ptr(error_word, dev))
+    _check(_lib.cb_kv_append_q8(ctypes.byref(a), st))
+    return q_out if q is not None else None
 
 
 def paged_attention_q8(q, k_cache, v_cache, k_scales, v_scales, cu_seqlens_q, seq_lens,
@@ -769,29 +816,24 @@ def paged_attention_q8(q, k_cache, v_cache, k_scales, v_scales, cu_seqlens_q, se
                        sliding_window: int = 0, after_append: bool = False):
     """cb_paged_attention_q8: ``paged_attention`` over an 8-bit cache (see
     ``kv_append_q8``); q and out are bf16 or f32."""
-    torch = _torch()
-    _need_cuda(q)
-    nb, hkv, bs, d, ss = _need_q8(k_cache, v_cache, k_scales, v_scales)
+    dev, st = _launch_on(q, stream)
+    (nb, hkv, bs, d), ss, kc, vc, ks, vs = _q8(dev, k_cache, v_cache, k_scales, v_scales)
     if out is None:
-        out = torch.empty_like(q)
-    _need_cuda(out)
-    T, hq, _ = q.shape
-    R = seq_lens.shape[0]
-    if q.shape[2] != d or out.shape != q.shape or out.dtype != q.dtype:
-        raise ValueError(f"q and out must be [T, Hq, {d}] of one type")
-    _need_i32("cu_seqlens_q", cu_seqlens_q, (R + 1,))
-    _need_i32("seq_lens", seq_lens, (R,))
-    _need_i32("block_tables", block_tables, (R, block_tables.shape[-1]))
+        out = _torch().empty_like(q)
+    T, hq = q.shape[0], q.shape[1]
+    qp = _rows3("q", q, dev, q.dtype, T, hq, d)
+    op = _rows3("out", out, dev, q.dtype, T, hq, d)
+    R, W = block_tables.shape
+    cu, seq, bt = _i32(dev, (("cu_seqlens_q", cu_seqlens_q, R + 1), ("seq_lens", seq_lens, R),
+                             ("block_tables", block_tables, R * W)))
     if R > workspace.max_reqs:
         raise ValueError("workspace sized for fewer requests")
-    _need_one_device(q, out, k_cache, cu_seqlens_q, seq_lens, block_tables, workspace.buf)
-    a = cb_attention_args(q.data_ptr(), out.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
-                          cu_seqlens_q.data_ptr(), seq_lens.data_ptr(), block_tables.data_ptr(),
-                          R, num_decodes, T, max_q_len, max_seq_len, nb, block_tables.shape[1],
-                          bs, hq, hkv, d, float(scale), _dtype_code(q), workspace.ptr,
-                          workspace.nbytes, int(sliding_window), int(bool(after_append)))
-    _check(_lib.cb_paged_attention_q8(ctypes.byref(a), k_scales.data_ptr(), v_scales.data_ptr(), ss,
-                                      _stream_ptr(stream)))
+    if workspace.buf.get_device() != dev:
+        raise ValueError("tensors live on different devices")
+    a = cb_attention_args(qp, op, kc, vc, cu, seq, bt, R, num_decodes, T, max_q_len, max_seq_len,
+                          nb, W, bs, hq, hkv, d, scale, _dtype_code(q), workspace.ptr,
+                          workspace.nbytes, sliding_window, 1 if after_append else 0)
+    _check(_lib.cb_paged_attention_q8(ctypes.byref(a), ks, vs, ss, st))
     return out
 
 
