@@ -64,6 +64,14 @@ using namespace decode;
 constexpr int kWarps = 8;
 constexpr int kMaxHeads = 16;  // query heads of an item
 constexpr int kPair = 2;       // pages of a stage
+// An item costs a few microseconds beside its pages (its queries, its place
+// in the plan, its partial and ticket), and joining a row's splits about one
+// for 8 of them.  So a step with few pages to a warp is cut into one item
+// each (8 requests of up to 512 tokens: 13.6 us, 19 with two phases), and a
+// long row into at most 64 splits and the last phase's (one request of 32k
+// tokens: 46 us, 65 without the limit).
+constexpr int kSinglePages = 8;
+constexpr int kMaxSplits = 64;
 // weight exponent at the reference, which moves when passed by more than the
 // lag (float32: exponents near 0 are the most exact)
 template <typename T> constexpr float kTop = 7.f;
@@ -186,6 +194,7 @@ __device__ __noinline__ void merge_splits(const Params& p, int h0, int heads, in
         o[h].x *= a_old; o[h].y *= a_old; o[h].z *= a_old; o[h].w *= a_old;
         M[h] = Mn;
       }
+      // (more in flight at once takes registers that the caller would spill)
 #pragma unroll 4
       for (int k = 0; k < cnt; ++k) {
 #pragma unroll
@@ -261,7 +270,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_kernel(const __grid_con
 
   const SplitPlan plan = plan_splits<kWarps>(
       PlanRows{p.seq_lens, p.cu_seqlens_q, p.row_begin, p.num_rows, p.num_tokens, W, units, win,
-               p.max_slots, p.pdl_mode == 2 ? kItemsABeside : kItemsA, p.error_word},
+               p.max_slots, p.pdl_mode == 2 ? kItemsABeside : kItemsA, p.error_word, kPair, kMaxSplits, kSinglePages},
       nwarps, plan_a, plan_b, row_len, row_tok);
   const int spa0 = plan.spa, spb0 = plan.spb;
   const int num_a = plan_a[p.num_rows];

@@ -50,6 +50,13 @@ struct PlanRows {
   int32_t max_slots;    // partial slots available (>= 2 * num_rows)
   int32_t items_a;      // phase-A items per warp (target)
   uint32_t* error_word;
+  // Splits are whole multiples of `step` pages.  max_splits > 0: the
+  // longest row has at most that many phase-A splits, and half as many in
+  // phase B; and with at most single_pages pages to a warp there is one phase,
+  // of one item to a warp (and that limit).
+  int32_t step = 1;
+  int32_t max_splits = 0;
+  int32_t single_pages = 0;
 };
 
 struct SplitPlan {
@@ -65,7 +72,11 @@ __device__ __forceinline__ SplitPlan plan_splits(const PlanRows& in, int nwarps,
                                                  int32_t* plan_b, int32_t* row_len,
                                                  int32_t* row_tok) {
   __shared__ int32_t s_red[2][kMaxWarps];
-  __shared__ int32_t s_spa, s_spb;
+  __shared__ int32_t s_spa, s_spb, s_longest;
+  if (in.max_splits > 0) {
+    if (threadIdx.x == 0) s_longest = 0;
+    __syncthreads();
+  }
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int nthreads = nwarps * 32;
@@ -94,6 +105,7 @@ __device__ __forceinline__ SplitPlan plan_splits(const PlanRows& in, int nwarps,
     row_len[i] = L;
     row_tok[i] = q0;
     my_pages += pages;
+    if (in.max_splits > 0) atomicMax(&s_longest, pages);
   }
   for (int o = 16; o > 0; o >>= 1) my_pages += __shfl_xor_sync(0xffffffffu, my_pages, o);
   if (lane == 0) s_red[0][warp] = (int32_t)(my_pages < 0x3fffffff ? my_pages : 0x3fffffff);
@@ -109,6 +121,20 @@ __device__ __forceinline__ SplitPlan plan_splits(const PlanRows& in, int nwarps,
     int64_t spb = (units_b + workers * kItemsB - 1) / (workers * kItemsB);
     if (spa < kMinSplitPages) spa = kMinSplitPages;
     if (spb < 1) spb = 1;
+    if (in.max_splits > 0) {
+      const int64_t least = (s_longest + in.max_splits - 1) / in.max_splits;
+      if (units <= workers * in.single_pages) {
+        spb = (units + workers - 1) / workers;
+        if (spb < least) spb = least;
+        spa = 1 << 20;
+      } else {
+        if (spa < least) spa = least;
+        const int64_t tail = (s_longest / kTailDiv + spa) * 2 / in.max_splits;
+        if (spb < tail) spb = tail;
+      }
+    }
+    spa = (spa + in.step - 1) / in.step * in.step;
+    spb = (spb + in.step - 1) / in.step * in.step;
     s_spa = (int32_t)(spa < (1 << 20) ? spa : (1 << 20));
     s_spb = (int32_t)(spb < (1 << 20) ? spb : (1 << 20));
   }
