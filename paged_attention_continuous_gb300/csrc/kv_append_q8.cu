@@ -20,6 +20,8 @@
 // block's scale) small ones.
 #include <cuda_runtime.h>
 
+#include <algorithm>
+
 #include "cb_error.h"
 #include "launch_common.h"
 #include "q8.cuh"
@@ -51,40 +53,42 @@ struct Params {
   int64_t num_slots;
   int32_t num_tokens, tokens_per_cta;
   int32_t num_kv_heads;
-  const void* q;
-  void* q_out;
-  int32_t num_q_heads;  // 0: no q
+  rope::Rows q_rows;    // heads 0: no q
   uint32_t* error_word;
 };
 
 // Rotate one lane's N elements of a row of D (element offset `at`), whose
 // partners in the half layout lie in lane `at` +- rot / 2 of the same row.
+// cs: the token's angles as rope::angle_at has them.
 template <int kRope, int N>
 __device__ __forceinline__ void rotate_lane(float* x, int at, int rot, int lane, const float2* cs) {
+  constexpr int kPairs = rope::unit_pairs<N, kRope == kHalf>();
+  const int stride = rot / 2 / kPairs;
   if constexpr (kRope == kHalf) {
     const int half = rot / 2;
     const bool lo = at < half, in = at < rot;
     const int partner = lane + (in ? (lo ? half : -half) / N : 0);
-    const float2* c = cs + (in ? (lo ? at : at - half) : 0);
+    const float2* c = cs + (in ? (lo ? at : at - half) / N : 0);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const float y = __shfl_sync(0xffffffffu, x[i], partner);
       if (in) {
         float a = lo ? x[i] : y, b = lo ? y : x[i];
-        rope::rotate(a, b, c[i]);
+        rope::rotate(a, b, c[i * stride]);
         x[i] = lo ? a : b;
       }
     }
   } else {
     if (at < rot) {
 #pragma unroll
-      for (int i = 0; i < N; i += 2) rope::rotate(x[i], x[i + 1], cs[at / 2 + i / 2]);
+      for (int i = 0; i < N; i += 2) rope::rotate(x[i], x[i + 1], cs[at / N + i / 2 * stride]);
     }
   }
 }
 
 template <typename T, int D, int kRope>
-__global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(kThreads, D * sizeof(T) == 512 ? 2 : kRope == kNoRope ? 4 : 3)
+    append_kernel(const __grid_constant__ Params p) {
   constexpr int N = Vec<T>::kN;             // elements of a lane
   constexpr int kLanes = D / N;             // lanes of a row
   constexpr int kRows = 32 / kLanes;        // rows of a warp at once
@@ -122,7 +126,9 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
       if (t >= p.num_tokens) break;
       const int over = tl - (p.tokens_per_cta - 1);
       if (over > 0 && (last < 0 || (last & 15) + over > 15 || slots[1 + tl] != last + over)) continue;
-      cs[i] = rope::turn_of(p.plan.turns[i - tl * pairs], p.positions[t], p.plan.amplitude, false);
+      const int pair = i - tl * pairs;
+      cs[tl * pairs + rope::angle_at<N, kRope == kHalf>(pair, pairs)] =
+          rope::turn_of(p.plan.turns[pair], p.positions[t], p.plan.amplitude, false);
     }
     __syncthreads();
   }
@@ -130,7 +136,10 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
   const int sub = lane / kLanes, at = (lane - sub * kLanes) * N;  // row of a step, element offset
   const int Hkv = p.num_kv_heads;
   const int tokens = min(p.tokens_per_cta, p.num_tokens - t0);
-  for (int task = warp; task < tokens * Hkv * 2; task += kWarps) {
+  // tasks (token, head of K or V), dealt over the warps of the CTAs that
+  // share these tokens
+  const int worker = (int)blockIdx.y * kWarps + warp, workers = (int)gridDim.y * kWarps;
+  for (int task = worker; task < tokens * Hkv * 2; task += workers) {
     const int tl = task / (Hkv * 2), w = task - tl * (Hkv * 2);
     const int slot = slots[1 + tl], before = slots[tl];
     if (slot < 0) continue;
@@ -155,21 +164,26 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
       raw[i] = row < count ? __ldg(reinterpret_cast<const uint4*>(src + (int64_t)row * Hkv * D))
                            : make_uint4(0, 0, 0, 0);
     }
-    float x[kSteps][N];
+    // the values are unpacked (and turned) twice, for their largest magnitude
+    // and for their codes: kept in between, they would take twice the
+    // registers of the raw ones, and fewer CTAs would fit an SM
+    auto values = [&](int i, float* x) {
+      Vec<T>::load(raw[i], x);
+      if constexpr (kRope != kNoRope) {
+        if (!is_v) rotate_lane<kRope, N>(x, at, rot, lane, cs + (tl + min(i * kRows + sub, count - 1)) * pairs);
+      }
+    };
     float amax = 0.f;
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
-      Vec<T>::load(raw[i], x[i]);
-      if constexpr (kRope != kNoRope) {
-        if (!is_v && i * kRows < count) {
-          const int row = min(i * kRows + sub, count - 1);
-          rotate_lane<kRope, N>(x[i], at, rot, lane, cs + (tl + row) * pairs);
-        }
-      }
+      if (i * kRows < count) {
+        float x[N];
+        values(i, x);
 #pragma unroll
-      for (int e = 0; e < N; ++e) {
-        const float m = fabsf(x[i][e]);
-        amax = m <= 3.402823466e38f ? fmaxf(amax, m) : amax;  // not an infinity, not NaN
+        for (int e = 0; e < N; ++e) {
+          const float m = fabsf(x[e]);
+          amax = m <= 3.402823466e38f ? fmaxf(amax, m) : amax;  // not an infinity, not NaN
+        }
       }
     }
 #pragma unroll
@@ -191,15 +205,17 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
     const float f = q8::exp2i(-e);
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
-      const int row = i * kRows + sub;
-      if (row < count) {
+      if (i * kRows < count) {
+        float x[N];
+        values(i, x);
+        const int row = i * kRows + sub;
         uint8_t* dst = page + (off + row) * D + at;
-        const uint32_t lo = q8::codes2(x[i][0] * f, x[i][1] * f) | (q8::codes2(x[i][2] * f, x[i][3] * f) << 16);
+        const uint32_t lo = q8::codes2(x[0] * f, x[1] * f) | (q8::codes2(x[2] * f, x[3] * f) << 16);
         if constexpr (N == 8) {
-          const uint32_t hi = q8::codes2(x[i][4] * f, x[i][5] * f) | (q8::codes2(x[i][6] * f, x[i][7] * f) << 16);
-          *reinterpret_cast<uint2*>(dst) = make_uint2(lo, hi);
+          const uint32_t hi = q8::codes2(x[4] * f, x[5] * f) | (q8::codes2(x[6] * f, x[7] * f) << 16);
+          if (row < count) *reinterpret_cast<uint2*>(dst) = make_uint2(lo, hi);
         } else {
-          *reinterpret_cast<uint32_t*>(dst) = lo;
+          if (row < count) *reinterpret_cast<uint32_t*>(dst) = lo;
         }
       }
     }
@@ -207,33 +223,48 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
   }
 
   if constexpr (kRope != kNoRope) {
-    // q of this CTA's tokens, kRows head rows to a warp
-    const int rows = tokens * p.num_q_heads;
-    for (int r0 = warp * kRows; r0 < rows; r0 += kWarps * kRows) {
-      const int row = min(r0 + sub, rows - 1);
-      const int tl = row / p.num_q_heads;
-      const int64_t o = ((int64_t)t0 * p.num_q_heads + row) * D + at;
-      float x[N];
-      Vec<T>::load(*reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) + o), x);
-      rotate_lane<kRope, N>(x, at, rot, lane, cs + tl * pairs);
-      if (r0 + sub < rows) *reinterpret_cast<uint4*>(static_cast<T*>(p.q_out) + o) = Vec<T>::store(x);
+    // q of this CTA's tokens, a unit of the rows to a thread
+    constexpr int kAhead = 2;
+    const uint32_t items = (uint32_t)tokens * p.q_rows.heads * p.q_rows.units;
+    const uint32_t step = gridDim.y * kThreads;
+    for (uint32_t n = blockIdx.y * kThreads + threadIdx.x; n < items; n += kAhead * step) {
+      rope::Unit<T, N> w[kAhead];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i)
+        if (n + i * step < items) rope::load_unit<T, N, kRope == kHalf>(p.q_rows, t0, n + i * step, w[i]);
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i)
+        if (n + i * step < items)
+          rope::store_unit<T, N, kRope == kHalf>(cs, pairs / rope::unit_pairs<N, kRope == kHalf>(), w[i]);
     }
   }
 }
 
 template <typename T, int D, int kRope>
-cb_status launch(const Params& p, cudaStream_t stream) {
+cb_status launch(Params& p, cudaStream_t stream) {
+  if constexpr (kRope != kNoRope) {
+    rope::Rows& r = p.q_rows;
+    if (r.heads > 0) {
+      rope::cut_rows(&r, Vec<T>::kN, kRope == kHalf);
+      const uint64_t items = (uint64_t)p.tokens_per_cta * r.heads * r.units;
+      if (items * (uint64_t)(r.units > r.heads ? r.units : r.heads) >= 0x100000000ull)
+        return fail(CB_ERR_UNSUPPORTED, "cb_kv_append_q8: %d query heads", r.heads);
+    }
+  }
   const int64_t ctas = ((int64_t)p.num_tokens + p.tokens_per_cta - 1) / p.tokens_per_cta;
   const size_t smem = kRope == kNoRope ? 0
                                        : (size_t)(p.tokens_per_cta + q8::kPage - 1) * (p.plan.rot_dim / 2) * sizeof(float2);
-  append_kernel<T, D, kRope><<<(unsigned)ctas, kThreads, smem, stream>>>(p);
+  // CTAs that share the same tokens: one for every 8 (head of K or V)s, a warp
+  // for each, so that a run's heads are written side by side
+  const int share = std::min(std::max(p.num_kv_heads * 2 / kWarps, 1), 8);
+  append_kernel<T, D, kRope><<<dim3((unsigned)ctas, (unsigned)share), kThreads, smem, stream>>>(p);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return fail(CB_ERR_CUDA, "cb_kv_append_q8 launch: %s", cudaGetErrorString(e));
   return CB_OK;
 }
 
 template <typename T, int D>
-cb_status dispatch(const Params& p, bool with_rope, cudaStream_t stream) {
+cb_status dispatch(Params& p, bool with_rope, cudaStream_t stream) {
   if (!with_rope) return launch<T, D, kNoRope>(p, stream);
   return p.plan.layout == CB_ROPE_HALF ? launch<T, D, kHalf>(p, stream)
                                        : launch<T, D, kInterleaved>(p, stream);
@@ -295,9 +326,14 @@ extern "C" cb_status cb_kv_append_q8(const cb_append_q8_args* args, cb_stream_t 
   p.num_slots = (int64_t)a.num_blocks * a.block_size;
   p.num_tokens = a.num_tokens;
   p.num_kv_heads = a.num_kv_heads;
-  p.q = a.q;
-  p.q_out = a.q_out;
-  p.num_q_heads = a.q ? a.num_q_heads : 0;
+  if (a.q) {
+    p.q_rows.head_dim = a.head_dim;
+    p.q_rows.rot_dim = p.plan.rot_dim;
+    p.q_rows.hq = p.q_rows.heads = a.num_q_heads;
+    p.q_rows.q = a.q;
+    p.q_rows.q_out = a.q_out;
+    p.q_rows.q_stride = p.q_rows.q_out_stride = (int64_t)a.num_q_heads * a.head_dim;
+  }
   p.error_word = a.error_word;
   p.tokens_per_cta = a.num_tokens <= 1024 ? 1 : kMaxTokens;
   const bool f32 = a.dtype == CB_DTYPE_F32;

@@ -70,5 +70,124 @@ __device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162f
 __device__ __forceinline__ void from_float(float* p, float x) { *p = x; }
 __device__ __forceinline__ void from_float(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
 
+// ---- rows of q (and k) as units of work ------------------------------------
+// The rows of a few tokens, cut into units that one thread moves: rot_units
+// per head row that rotate, then units that are only copied.
+struct Rows {
+  int32_t head_dim, rot_dim;
+  int32_t hq, heads;                  // heads of q (0 without q), of q and k together
+  int32_t units, rot_units;           // of one head row
+  uint32_t units_magic, heads_magic;  // ceil(2^32 / x)
+  const void* q;
+  void* q_out;
+  const void* k;
+  void* k_out;
+  int64_t q_stride, q_out_stride, k_stride, k_out_stride;  // elements from token to token
+};
+
+// Fills units, rot_units and the magics for units of N elements.
+inline void cut_rows(Rows* r, int n, bool half) {
+  r->rot_units = half ? r->rot_dim / 2 / n : n > 1 ? r->rot_dim / n : r->rot_dim / 2;
+  r->units = r->rot_units + (r->head_dim - r->rot_dim) / n;
+  auto magic = [](int d) { return d == 1 ? 0u : (uint32_t)((0x100000000ull + d - 1) / d); };
+  r->units_magic = magic(r->units);
+  r->heads_magic = magic(r->heads);
+}
+
+// Pairs of a unit of N elements, and where the angle of pair i lies in shared
+// memory: the i-th pairs of all units side by side, so that neighbouring
+// threads read neighbouring words.
+template <int N, bool kHalf>
+constexpr int unit_pairs() { return N == 1 || kHalf ? N : N / 2; }
+template <int N, bool kHalf>
+__device__ __forceinline__ int angle_at(int i, int pairs) {
+  constexpr int g = unit_pairs<N, kHalf>();
+  return i % g * (pairs / g) + i / g;
+}
+
+// n / d for n d < 2^32, magic = ceil(2^32 / d) (0 for d = 1)
+__device__ __forceinline__ uint32_t div_by(uint32_t n, uint32_t magic) {
+  return magic ? __umulhi(n, magic) : n;
+}
+
+// A unit of work: N elements at `a`, and their partners at `b` when it
+// rotates in the half layout (or N = 1, for rows that vectors do not fit: one
+// pair, or one element to copy).  pair < 0: a unit that is only copied.
+template <typename T, int N>
+struct Unit {
+  T* out;
+  int a, b, pair;
+  bool same;        // in place
+  uint4 x, y;       // N elements each, as they lie in memory (N = 1: one float)
+};
+
+template <typename T, int N, bool kHalf>
+__device__ __forceinline__ void load_unit(const Rows& p, int t0, uint32_t n, Unit<T, N>& w) {
+  const int D = p.head_dim, rot = p.rot_dim;
+  const uint32_t row = div_by(n, p.units_magic);
+  const int u = (int)(n - row * (uint32_t)p.units);
+  const uint32_t tl = div_by(row, p.heads_magic);
+  const int head = (int)(row - tl * (uint32_t)p.heads);
+  const int64_t t = t0 + (int)tl;
+  const T* in;
+  if (head < p.hq) {
+    in = static_cast<const T*>(p.q) + t * p.q_stride + (int64_t)head * D;
+    w.out = static_cast<T*>(p.q_out) + t * p.q_out_stride + (int64_t)head * D;
+  } else {
+    in = static_cast<const T*>(p.k) + t * p.k_stride + (int64_t)(head - p.hq) * D;
+    w.out = static_cast<T*>(p.k_out) + t * p.k_out_stride + (int64_t)(head - p.hq) * D;
+  }
+  w.same = in == w.out;
+  w.b = -1;
+  if (u >= p.rot_units) {
+    w.a = rot + (u - p.rot_units) * N;
+    w.pair = -1;
+  } else {
+    w.pair = (int)tl * (rot / 2) + u;  // the unit's first angle in shared memory
+    if (kHalf) {
+      w.a = u * N;
+      w.b = w.a + rot / 2;
+    } else if (N > 1) {
+      w.a = u * N;
+    } else {
+      w.a = 2 * u;
+      w.b = w.a + 1;
+    }
+  }
+  if constexpr (N > 1) {
+    w.x = *reinterpret_cast<const uint4*>(in + w.a);
+    if (kHalf && w.b >= 0) w.y = *reinterpret_cast<const uint4*>(in + w.b);
+  } else {
+    w.x.x = __float_as_uint(to_float(in[w.a]));
+    if (w.b >= 0) w.y.x = __float_as_uint(to_float(in[w.b]));
+  }
+}
+
+template <typename T, int N, bool kHalf>
+__device__ __forceinline__ void store_unit(const float2* cs, int stride, const Unit<T, N>& w) {
+  if (w.pair < 0 && w.same) return;  // in place: nothing to copy
+  if constexpr (N == 1) {
+    float x = __uint_as_float(w.x.x), y = __uint_as_float(w.y.x);
+    if (w.pair >= 0) rotate(x, y, cs[w.pair]);
+    from_float(w.out + w.a, x);
+    if (w.b >= 0) from_float(w.out + w.b, y);
+  } else if (w.pair < 0) {
+    *reinterpret_cast<uint4*>(w.out + w.a) = w.x;
+  } else {
+    float x[N], y[N];
+    Vec<T>::load(w.x, x);
+    if constexpr (kHalf) {
+      Vec<T>::load(w.y, y);
+#pragma unroll
+      for (int i = 0; i < N; ++i) rotate(x[i], y[i], cs[w.pair + i * stride]);
+      *reinterpret_cast<uint4*>(w.out + w.b) = Vec<T>::store(y);
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; i += 2) rotate(x[i], x[i + 1], cs[w.pair + i / 2 * stride]);
+    }
+    *reinterpret_cast<uint4*>(w.out + w.a) = Vec<T>::store(x);
+  }
+}
+
 }  // namespace rope
 }  // namespace cb
