@@ -9,15 +9,22 @@
 // of K or V: it holds the run's values in registers, takes their largest
 // magnitude, derives the exponent, and writes codes.  The block's old scale
 // is read beside the values; the old codes only if that scale has to grow
-// (a block's largest value is met early, so few appends do).
+// (a block's largest value is met early, so few appends do).  The runs of a
+// CTA's tokens are counted first and (run, head) dealt to the warps: dealt
+// by token instead, some warps wrote two runs one after the other while
+// others had none (8192 tokens below: 14.9 us).
 //
-// With a rotary plan, k turns in registers before its magnitude is taken,
-// and the same CTA rotates its tokens' q: the angles of a token are computed
-// once for all heads, and k is neither written nor read in between.
+// With a rotary plan, k turns in registers before its magnitude is taken, a
+// lane holding both elements of its pairs, and k is neither written nor read
+// in between.  CTAs of their own rotate the tokens' q: with q after k in the
+// same CTAs, or partners in two lanes and exchanged by shuffles, the call
+// below took 48 us.
 //
 // Every new element is read once and every code written once; HBM bounds
 // large calls and the launch with two dependent loads (slots, then the
-// block's scale) small ones.
+// block's scale) small ones.  Measured on the GPU alone, bf16, 8 heads of
+// 128: 8192 tokens 10.6 us (4.0 TB/s), 96 tokens with 32 heads of q turned
+// 4.5 us, 8192 tokens with 32 heads of q turned 33.5 us (4.6 TB/s).
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -37,6 +44,7 @@ using rope::Vec;
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxTokens = 16;  // tokens of a CTA
+constexpr int kPad = 8;         // angles left out behind a token's, so that rows side by side read other banks
 enum { kNoRope = -1, kHalf = CB_ROPE_HALF, kInterleaved = CB_ROPE_INTERLEAVED };
 
 struct Params {
@@ -53,55 +61,82 @@ struct Params {
   int64_t num_slots;
   int32_t num_tokens, tokens_per_cta;
   int32_t num_kv_heads;
+  // CTAs of the same tokens (grid y): kv_ctas for k, as many for v, and with
+  // q one for every q_tokens tokens
+  int32_t kv_ctas, q_tokens;
   rope::Rows q_rows;    // heads 0: no q
   uint32_t* error_word;
 };
 
-// Rotate one lane's N elements of a row of D (element offset `at`), whose
-// partners in the half layout lie in lane `at` +- rot / 2 of the same row.
-// cs: the token's angles as rope::angle_at has them.
-template <int kRope, int N>
-__device__ __forceinline__ void rotate_lane(float* x, int at, int rot, int lane, const float2* cs) {
-  constexpr int kPairs = rope::unit_pairs<N, kRope == kHalf>();
-  const int stride = rot / 2 / kPairs;
-  if constexpr (kRope == kHalf) {
-    const int half = rot / 2;
-    const bool lo = at < half, in = at < rot;
-    const int partner = lane + (in ? (lo ? half : -half) / N : 0);
-    const float2* c = cs + (in ? (lo ? at : at - half) / N : 0);
+// Rotates q: tokens t0 ... of one CTA, a unit of the rows to a thread.
+template <typename T, int kRope>
+__device__ __forceinline__ void rotate_q(const Params& p, int t0, int tokens, float2* cs) {
+  constexpr int N = Vec<T>::kN;
+  constexpr int kAhead = kRope == kHalf ? 2 : 4;  // 64 bytes of loads in flight per thread
+  const uint32_t items = (uint32_t)tokens * p.q_rows.heads * p.q_rows.units;
+  rope::Unit<T, N> w[kAhead];
+  uint32_t n = threadIdx.x;
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const float y = __shfl_sync(0xffffffffu, x[i], partner);
-      if (in) {
-        float a = lo ? x[i] : y, b = lo ? y : x[i];
-        rope::rotate(a, b, c[i * stride]);
-        x[i] = lo ? a : b;
-      }
-    }
-  } else {
-    if (at < rot) {
+  for (int i = 0; i < kAhead; ++i)
+    if (n + i * kThreads < items) rope::load_unit<T, N, kRope == kHalf>(p.q_rows, t0, n + i * kThreads, w[i]);
+  const int pairs = p.plan.rot_dim / 2;
+  for (int i = threadIdx.x; i < tokens * pairs; i += kThreads) {
+    const int tl = i / pairs, pair = i - tl * pairs;
+    cs[tl * pairs + rope::angle_at<N, kRope == kHalf>(pair, pairs)] =
+        rope::turn_of(p.plan.turns[pair], p.positions[t0 + tl], p.plan.amplitude, false);
+  }
+  __syncthreads();
+  while (true) {
 #pragma unroll
-      for (int i = 0; i < N; i += 2) rope::rotate(x[i], x[i + 1], cs[at / N + i / 2 * stride]);
-    }
+    for (int i = 0; i < kAhead; ++i)
+      if (n + i * kThreads < items)
+        rope::store_unit<T, N, kRope == kHalf>(cs, pairs / rope::unit_pairs<N, kRope == kHalf>(), w[i]);
+    n += kAhead * kThreads;
+    if (n >= items) break;
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+      if (n + i * kThreads < items) rope::load_unit<T, N, kRope == kHalf>(p.q_rows, t0, n + i * kThreads, w[i]);
   }
 }
 
+// The codes of N values, in one store.
+template <int N>
+__device__ __forceinline__ void store_codes(uint8_t* dst, const float (&x)[N], float f) {
+  const uint32_t lo = q8::codes2(x[0] * f, x[1] * f) | (q8::codes2(x[2] * f, x[3] * f) << 16);
+  if constexpr (N == 8)
+    *reinterpret_cast<uint2*>(dst) =
+        make_uint2(lo, q8::codes2(x[4] * f, x[5] * f) | (q8::codes2(x[6] * f, x[7] * f) << 16));
+  else
+    *reinterpret_cast<uint32_t*>(dst) = lo;
+}
+
+// CTAs an SM should hold: four, where the registers of a run allow it
 template <typename T, int D, int kRope>
-__global__ void __launch_bounds__(kThreads, D * sizeof(T) == 512 ? 2 : kRope == kNoRope ? 4 : 3)
+constexpr int resident() { return sizeof(T) == 2 ? 4 : D == 128 ? 2 : kRope == kNoRope ? 4 : 3; }
+
+template <typename T, int D, int kRope>
+__global__ void __launch_bounds__(kThreads, resident<T, D, kRope>())
     append_kernel(const __grid_constant__ Params p) {
-  constexpr int N = Vec<T>::kN;             // elements of a lane
-  constexpr int kLanes = D / N;             // lanes of a row
-  constexpr int kRows = 32 / kLanes;        // rows of a warp at once
-  constexpr int kSteps = q8::kPage / kRows; // steps of a full block
-  static_assert(kLanes <= 32, "a row must fit a warp");
+  constexpr int N = Vec<T>::kN;              // elements of a vector; a lane holds two of a row
+  constexpr int kLanes = D / N / 2;          // lanes of a row
+  constexpr int kRows = 32 / kLanes;         // rows of a warp at once
+  constexpr int kSteps = q8::kPage / kRows;  // steps of a full block
   // slots of this CTA's tokens, of the one before and of those a run that
   // starts here can reach
   __shared__ int32_t slots[1 + kMaxTokens + q8::kPage];
-  extern __shared__ float2 cs[];            // [tokens_per_cta + 15][rot_dim / 2]
+  extern __shared__ float2 cs[];             // [tokens_per_cta + 15][rot_dim / 2 + kPad]
   // the attention launch that follows (when it asks for it) may start now;
   // it reads the cache only after this grid has completed
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int t0 = (int)blockIdx.x * p.tokens_per_cta;
+  if constexpr (kRope != kNoRope) {
+    if ((int)blockIdx.y >= 2 * p.kv_ctas) {
+      const int q0 = t0 + ((int)blockIdx.y - 2 * p.kv_ctas) * p.q_tokens;
+      if (q0 < p.num_tokens) rotate_q<T, kRope>(p, q0, min(p.q_tokens, p.num_tokens - q0), cs);
+      return;
+    }
+  }
+  const bool is_v = (int)blockIdx.y >= p.kv_ctas;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int reach = p.tokens_per_cta + q8::kPage - 1;
   if (threadIdx.x < reach + 1) {
@@ -114,80 +149,133 @@ __global__ void __launch_bounds__(kThreads, D * sizeof(T) == 512 ? 2 : kRope == 
     }
     slots[threadIdx.x] = s;
   }
-  const int rot = kRope == kNoRope ? 0 : p.plan.rot_dim;
-  const int pairs = rot / 2;
   __syncthreads();
-  if constexpr (kRope != kNoRope) {
-    // angles of this CTA's tokens, and of the tokens behind them that belong
-    // to its last run
-    const int last = slots[p.tokens_per_cta];
-    for (int i = threadIdx.x; i < reach * pairs; i += kThreads) {
-      const int tl = i / pairs, t = t0 + tl;
-      if (t >= p.num_tokens) break;
-      const int over = tl - (p.tokens_per_cta - 1);
-      if (over > 0 && (last < 0 || (last & 15) + over > 15 || slots[1 + tl] != last + over)) continue;
-      const int pair = i - tl * pairs;
-      cs[tl * pairs + rope::angle_at<N, kRope == kHalf>(pair, pairs)] =
-          rope::turn_of(p.plan.turns[pair], p.positions[t], p.plan.amplitude, false);
+  // the runs that start at this CTA's tokens: lane i looks at the i-th token
+  const int tokens = min(p.tokens_per_cta, p.num_tokens - t0);
+  bool starts = false;
+  if (lane < tokens) {
+    const int slot = slots[1 + lane], before = slots[lane];
+    const bool inside = slot % q8::kPage != 0 && before == slot - 1;
+    starts = slot >= 0 && !inside;
+    if (starts && before >= 0 && before / q8::kPage == slot / q8::kPage) {  // neighbours out of order
+      set_error(p.error_word, CB_DEVERR_SLOT_ORDER);
+      starts = false;
     }
-    __syncthreads();
+  }
+  const uint32_t run_starts = __ballot_sync(0xffffffffu, starts);
+  const int nth = __popc(run_starts & ((1u << lane) - 1u));  // of the run that starts at the lane's token
+  // tasks (run, head), dealt over the warps of the CTAs that share these tokens
+  const int Hkv = p.num_kv_heads;
+  const int num_tasks = __popc(run_starts) * Hkv;
+  const int worker0 = ((int)blockIdx.y - (is_v ? p.kv_ctas : 0)) * kWarps;
+  if (worker0 >= num_tasks) return;
+  const int pairs = kRope == kNoRope ? 0 : p.plan.rot_dim / 2;
+  const int angles = pairs + kPad;  // of a token
+  if constexpr (kRope != kNoRope) {
+    if (!is_v) {
+      // angles of this CTA's tokens, and of the tokens behind them that
+      // belong to its last run
+      const int last = slots[p.tokens_per_cta];
+      for (int i = threadIdx.x; i < reach * pairs; i += kThreads) {
+        const int tl = i / pairs, t = t0 + tl;
+        if (t >= p.num_tokens) break;
+        const int over = tl - (p.tokens_per_cta - 1);
+        if (over > 0 && (last < 0 || (last & 15) + over > 15 || slots[1 + tl] != last + over)) continue;
+        const int pair = i - tl * pairs;
+        cs[tl * angles + rope::angle_at<N, kRope == kHalf>(pair, pairs)] =
+            rope::turn_of(p.plan.turns[pair], p.positions[t], p.plan.amplitude, false);
+      }
+      __syncthreads();
+    }
   }
 
-  const int sub = lane / kLanes, at = (lane - sub * kLanes) * N;  // row of a step, element offset
-  const int Hkv = p.num_kv_heads;
-  const int tokens = min(p.tokens_per_cta, p.num_tokens - t0);
-  // tasks (token, head of K or V), dealt over the warps of the CTAs that
-  // share these tokens
-  const int worker = (int)blockIdx.y * kWarps + warp, workers = (int)gridDim.y * kWarps;
-  for (int task = worker; task < tokens * Hkv * 2; task += workers) {
-    const int tl = task / (Hkv * 2), w = task - tl * (Hkv * 2);
-    const int slot = slots[1 + tl], before = slots[tl];
-    if (slot < 0) continue;
-    const int off = slot & (q8::kPage - 1), block = slot >> 4;
-    if (off > 0 && before == slot - 1) continue;              // inside a run
-    if (before >= 0 && (before >> 4) == block) {              // neighbours out of order
-      if (w == 0 && lane == 0) set_error(p.error_word, CB_DEVERR_SLOT_ORDER);
-      continue;
+  // The lane's vectors of a row, at elements a and b: two halves of a row,
+  // or for k in the half layout a vector of first elements and that of their
+  // partners, then (where the row is not turned) two neighbours.
+  const int sub = lane / kLanes, j = lane - sub * kLanes;
+  int a = j * N, b = a + D / 2;
+  if (kRope == kHalf && !is_v) {
+    b = a + pairs;
+    if (a >= pairs) {
+      a += a;
+      b = a + N;
     }
+  }
+  const int64_t row_stride = (int64_t)Hkv * D;
+  for (int task = worker0 + warp; task < num_tasks; task += p.kv_ctas * kWarps) {
+    const int run = task / Hkv, h = task - run * Hkv;
+    const int tl = __ffs(__ballot_sync(0xffffffffu, starts && nth == run)) - 1;
+    const int slot = slots[1 + tl];
+    const int off = slot & (q8::kPage - 1), block = slot >> 4;
     // tokens of the run: lane i looks at the i-th slot
     const bool follows = lane < q8::kPage - off && slots[1 + tl + (lane < q8::kPage ? lane : 0)] == slot + lane;
     const int count = __ffs(~__ballot_sync(0xffffffffu, follows)) - 1;
-    const bool is_v = w >= Hkv;
-    const int h = is_v ? w - Hkv : w;
-    const T* src = static_cast<const T*>(is_v ? p.v_new : p.k_new) + ((int64_t)(t0 + tl) * Hkv + h) * D + at;
+    const T* src = static_cast<const T*>(is_v ? p.v_new : p.k_new) + (t0 + tl) * row_stride + h * D;
     uint8_t* scale = (is_v ? p.v_scales : p.k_scales) + (int64_t)block * p.scale_stride + h;
     const int was = off > 0 ? q8::exp_of(*scale) : q8::kMinExp;
-    uint4 raw[kSteps];
+    uint4 raw[kSteps][2];
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
       const int row = i * kRows + sub;
-      raw[i] = row < count ? __ldg(reinterpret_cast<const uint4*>(src + (int64_t)row * Hkv * D))
-                           : make_uint4(0, 0, 0, 0);
+      const T* r = src + row * row_stride;
+      raw[i][0] = row < count ? __ldg(reinterpret_cast<const uint4*>(r + a)) : make_uint4(0, 0, 0, 0);
+      raw[i][1] = row < count ? __ldg(reinterpret_cast<const uint4*>(r + b)) : make_uint4(0, 0, 0, 0);
     }
     // the values are unpacked (and turned) twice, for their largest magnitude
     // and for their codes: kept in between, they would take twice the
     // registers of the raw ones, and fewer CTAs would fit an SM
-    auto values = [&](int i, float* x) {
-      Vec<T>::load(raw[i], x);
+    auto values = [&](int i, float* x, float* y) {
+      Vec<T>::load(raw[i][0], x);
+      Vec<T>::load(raw[i][1], y);
       if constexpr (kRope != kNoRope) {
-        if (!is_v) rotate_lane<kRope, N>(x, at, rot, lane, cs + (tl + min(i * kRows + sub, count - 1)) * pairs);
-      }
-    };
-    float amax = 0.f;
+        if (!is_v) {
+          const float2* c = cs + (tl + min(i * kRows + sub, count - 1)) * angles + j;
+          const int stride = pairs / rope::unit_pairs<N, kRope == kHalf>();
+          if constexpr (kRope == kHalf) {
+            if (j < stride) {
 #pragma unroll
-    for (int i = 0; i < kSteps; ++i) {
-      if (i * kRows < count) {
-        float x[N];
-        values(i, x);
+              for (int e = 0; e < N; ++e) rope::rotate(x[e], y[e], c[e * stride]);
+            }
+          } else {
+            if (j < stride) {
 #pragma unroll
-        for (int e = 0; e < N; ++e) {
-          const float m = fabsf(x[e]);
-          amax = m <= 3.402823466e38f ? fmaxf(amax, m) : amax;  // not an infinity, not NaN
+              for (int e = 0; e < N; e += 2) rope::rotate(x[e], x[e + 1], c[e / 2 * stride]);
+            }
+            if (j + kLanes < stride) {
+#pragma unroll
+              for (int e = 0; e < N; e += 2) rope::rotate(y[e], y[e + 1], c[e / 2 * stride + kLanes]);
+            }
+          }
         }
       }
-    }
+    };
+    // the largest finite magnitude: fmaxf passes over NaN, and infinities
+    // are rare enough for a second look at all values
+    auto largest = [&](float above) {
+      float amax = 0.f;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+      for (int i = 0; i < kSteps; ++i) {
+        if (i * kRows < count) {
+          float x[N], y[N];
+          values(i, x, y);
+#pragma unroll
+          for (int e = 0; e < N; ++e) {
+            const float m = fabsf(x[e]), n = fabsf(y[e]);
+            if (above > 0.f) {
+              amax = m < above ? fmaxf(amax, m) : amax;
+              amax = n < above ? fmaxf(amax, n) : amax;
+            } else {
+              amax = fmaxf(amax, fmaxf(m, n));
+            }
+          }
+        }
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+      return amax;
+    };
+    float amax = largest(0.f);
+    if (isinf(amax)) amax = largest(amax);
     const int e = max(q8::exp_for(amax), was);
     uint8_t* page = (is_v ? p.v_cache : p.k_cache) + ((int64_t)block * Hkv + h) * (q8::kPage * D);
     if (off > 0 && e > was) {
@@ -206,37 +294,17 @@ __global__ void __launch_bounds__(kThreads, D * sizeof(T) == 512 ? 2 : kRope == 
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
       if (i * kRows < count) {
-        float x[N];
-        values(i, x);
+        float x[N], y[N];
+        values(i, x, y);
         const int row = i * kRows + sub;
-        uint8_t* dst = page + (off + row) * D + at;
-        const uint32_t lo = q8::codes2(x[0] * f, x[1] * f) | (q8::codes2(x[2] * f, x[3] * f) << 16);
-        if constexpr (N == 8) {
-          const uint32_t hi = q8::codes2(x[4] * f, x[5] * f) | (q8::codes2(x[6] * f, x[7] * f) << 16);
-          if (row < count) *reinterpret_cast<uint2*>(dst) = make_uint2(lo, hi);
-        } else {
-          if (row < count) *reinterpret_cast<uint32_t*>(dst) = lo;
+        uint8_t* dst = page + (off + row) * D;
+        if (row < count) {
+          store_codes(dst + a, x, f);
+          store_codes(dst + b, y, f);
         }
       }
     }
     if (lane == 0) *scale = (uint8_t)(e + 127);
-  }
-
-  if constexpr (kRope != kNoRope) {
-    // q of this CTA's tokens, a unit of the rows to a thread
-    constexpr int kAhead = 2;
-    const uint32_t items = (uint32_t)tokens * p.q_rows.heads * p.q_rows.units;
-    const uint32_t step = gridDim.y * kThreads;
-    for (uint32_t n = blockIdx.y * kThreads + threadIdx.x; n < items; n += kAhead * step) {
-      rope::Unit<T, N> w[kAhead];
-#pragma unroll
-      for (int i = 0; i < kAhead; ++i)
-        if (n + i * step < items) rope::load_unit<T, N, kRope == kHalf>(p.q_rows, t0, n + i * step, w[i]);
-#pragma unroll
-      for (int i = 0; i < kAhead; ++i)
-        if (n + i * step < items)
-          rope::store_unit<T, N, kRope == kHalf>(cs, pairs / rope::unit_pairs<N, kRope == kHalf>(), w[i]);
-    }
   }
 }
 
@@ -246,18 +314,20 @@ cb_status launch(Params& p, cudaStream_t stream) {
     rope::Rows& r = p.q_rows;
     if (r.heads > 0) {
       rope::cut_rows(&r, Vec<T>::kN, kRope == kHalf);
-      const uint64_t items = (uint64_t)p.tokens_per_cta * r.heads * r.units;
+      const uint64_t items = (uint64_t)std::min(p.tokens_per_cta, 4) * r.heads * r.units;
       if (items * (uint64_t)(r.units > r.heads ? r.units : r.heads) >= 0x100000000ull)
         return fail(CB_ERR_UNSUPPORTED, "cb_kv_append_q8: %d query heads", r.heads);
     }
   }
   const int64_t ctas = ((int64_t)p.num_tokens + p.tokens_per_cta - 1) / p.tokens_per_cta;
-  const size_t smem = kRope == kNoRope ? 0
-                                       : (size_t)(p.tokens_per_cta + q8::kPage - 1) * (p.plan.rot_dim / 2) * sizeof(float2);
-  // CTAs that share the same tokens: one for every 8 (head of K or V)s, a warp
-  // for each, so that a run's heads are written side by side
-  const int share = std::min(std::max(p.num_kv_heads * 2 / kWarps, 1), 8);
-  append_kernel<T, D, kRope><<<dim3((unsigned)ctas, (unsigned)share), kThreads, smem, stream>>>(p);
+  const size_t smem =
+      kRope == kNoRope ? 0 : (size_t)(p.tokens_per_cta + q8::kPage - 1) * (p.plan.rot_dim / 2 + kPad) * sizeof(float2);
+  // a warp for every head of a run, so that its heads are written side by
+  // side; 16 tokens mostly hold the starts of one or two runs
+  p.kv_ctas = std::min(std::max(p.num_kv_heads * (p.tokens_per_cta > 1 ? 2 : 1) / kWarps, 1), 16);
+  p.q_tokens = std::min(p.tokens_per_cta, 4);
+  const int q_ctas = p.q_rows.heads > 0 ? p.tokens_per_cta / p.q_tokens : 0;
+  append_kernel<T, D, kRope><<<dim3((unsigned)ctas, (unsigned)(2 * p.kv_ctas + q_ctas)), kThreads, smem, stream>>>(p);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return fail(CB_ERR_CUDA, "cb_kv_append_q8 launch: %s", cudaGetErrorString(e));
   return CB_OK;
