@@ -71,6 +71,7 @@ constexpr int kPair = 2;       // pages of a stage
 // long row into at most 64 splits and the last phase's (one request of 32k
 // tokens: 46 us, 65 without the limit).
 constexpr int kSinglePages = 8;
+constexpr int kSingleLeast = 4;
 constexpr int kMaxSplits = 64;
 // weight exponent at the reference, which moves when passed by more than the
 // lag (float32: exponents near 0 are the most exact)
@@ -158,11 +159,12 @@ __device__ __forceinline__ int row_token(int r) {
 // o = sum_s 2^(m_s - M) acc_s / sum_s 2^(m_s - M) l_s, in split order.
 // Not inlined: it is rare.  Its caller keeps nothing alive across the call.
 template <typename T, int D>
-__device__ __noinline__ void merge_splits(const Params& p, int h0, int heads, int s0, int n, int q0) {
+__device__ __noinline__ void merge_splits(const float* part_ml, const float* part_acc, void* out, int Hq,
+                                            int h0, int heads, int s0, int n, int q0) {
   const int lane = threadIdx.x & 31;
   constexpr int kV = D / 4;      // lanes that own 4 elements each
   constexpr int kH = 4;          // heads at once
-  const int Hq = p.num_q_heads;
+  constexpr int kB = 4;          // splits in flight: more takes registers that the caller would spill
   for (int hb = 0; hb < heads; hb += kH) {
     float M[kH], Ls[kH];
     float4 o[kH];
@@ -174,11 +176,25 @@ __device__ __noinline__ void merge_splits(const Params& p, int h0, int heads, in
     }
     for (int b0 = 0; b0 < n; b0 += 32) {
       const int cnt = min(32, n - b0);
+      float4 a[kB][kH];
+      auto load = [&](int k0) {
+#pragma unroll
+        for (int k = 0; k < kB; ++k)
+#pragma unroll
+          for (int h = 0; h < kH; ++h) {
+            const int head = h0 + min(hb + h, heads - 1);
+            a[k][h] = k0 + k < cnt && lane < kV
+                          ? __ldcg(reinterpret_cast<const float4*>(part_acc) +
+                                   ((int64_t)(s0 + b0 + k0 + k) * Hq + head) * kV + lane)
+                          : make_float4(0.f, 0.f, 0.f, 0.f);
+          }
+      };
+      load(0);  // beside the sums and references
       float wl[kH];
 #pragma unroll
       for (int h = 0; h < kH; ++h) {
         const int head = h0 + min(hb + h, heads - 1);
-        const float2 v = lane < cnt ? __ldcg(reinterpret_cast<const float2*>(p.part_ml) +
+        const float2 v = lane < cnt ? __ldcg(reinterpret_cast<const float2*>(part_ml) +
                                              (int64_t)(s0 + b0 + lane) * Hq + head)
                                     : make_float2(-INFINITY, 0.f);
         float bm = v.x;
@@ -194,25 +210,25 @@ __device__ __noinline__ void merge_splits(const Params& p, int h0, int heads, in
         o[h].x *= a_old; o[h].y *= a_old; o[h].z *= a_old; o[h].w *= a_old;
         M[h] = Mn;
       }
-      // (more in flight at once takes registers that the caller would spill)
-#pragma unroll 4
-      for (int k = 0; k < cnt; ++k) {
+#pragma unroll 1
+      for (int k0 = 0; k0 < cnt; k0 += kB) {
 #pragma unroll
-        for (int h = 0; h < kH; ++h) {
-          const int head = h0 + min(hb + h, heads - 1);
-          const float4 a = lane < kV ? __ldcg(reinterpret_cast<const float4*>(p.part_acc) +
-                                              ((int64_t)(s0 + b0 + k) * Hq + head) * kV + lane)
-                                     : make_float4(0.f, 0.f, 0.f, 0.f);
-          const float w = __shfl_sync(0xffffffffu, wl[h], k);
-          o[h].x += w * a.x; o[h].y += w * a.y; o[h].z += w * a.z; o[h].w += w * a.w;
-        }
+        for (int k = 0; k < kB; ++k)
+#pragma unroll
+          for (int h = 0; h < kH; ++h) {
+            const float w = __shfl_sync(0xffffffffu, wl[h], (k0 + k) & 31);
+            if (k0 + k < cnt) {
+              o[h].x += w * a[k][h].x; o[h].y += w * a[k][h].y; o[h].z += w * a[k][h].z; o[h].w += w * a[k][h].w;
+            }
+          }
+        if (k0 + kB < cnt) load(k0 + kB);
       }
     }
 #pragma unroll
     for (int h = 0; h < kH; ++h) {
       if (hb + h < heads && lane < kV) {
         const float inv = 1.f / Ls[h];
-        T* row = static_cast<T*>(p.out) + ((int64_t)q0 * Hq + h0 + hb + h) * D + 4 * lane;
+        T* row = static_cast<T*>(out) + ((int64_t)q0 * Hq + h0 + hb + h) * D + 4 * lane;
         if constexpr (sizeof(T) == 2) {
           *reinterpret_cast<uint2*>(row) = make_uint2(float2_to_bf16x2(o[h].x * inv, o[h].y * inv),
                                                       float2_to_bf16x2(o[h].z * inv, o[h].w * inv));
@@ -270,7 +286,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_kernel(const __grid_con
 
   const SplitPlan plan = plan_splits<kWarps>(
       PlanRows{p.seq_lens, p.cu_seqlens_q, p.row_begin, p.num_rows, p.num_tokens, W, units, win,
-               p.max_slots, p.pdl_mode == 2 ? kItemsABeside : kItemsA, p.error_word, kPair, kMaxSplits, kSinglePages},
+               p.max_slots, p.pdl_mode == 2 ? kItemsABeside : kItemsA, p.error_word, kPair, kMaxSplits, kSinglePages, kSingleLeast},
       nwarps, plan_a, plan_b, row_len, row_tok);
   const int spa0 = plan.spa, spb0 = plan.spb;
   const int num_a = plan_a[p.num_rows];
@@ -287,9 +303,12 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_kernel(const __grid_con
   const uint64_t pol = l2_policy_evict_first();
 
   // ---- dealing: the first item is dealt statically (item w of W warps),
-  // later ones are drawn from the counter, whose next value lane 0 keeps in
-  // flight; the item after the producer's current one is decoded, and its
-  // first block ids requested, one item early.  Beside a prefill grid every
+  // later ones are drawn from the counter.  Two steps before the producer
+  // reaches the end of its item it draws the next one, and one step before,
+  // it decodes that item and requests its first block ids: early enough that
+  // neither is waited for, and no earlier, since an item drawn is one that no
+  // idle warp can take (drawn with the item before, two ahead, most of the
+  // small items were dealt when the call began).  Beside a prefill grid every
   // item is drawn.
   const int items_a = num_a * units;
   // warp w of every CTA before warp w + 1 of any: when there are fewer large
@@ -298,8 +317,10 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_kernel(const __grid_con
   const uint32_t n_static =
       p.pdl_mode == 2 ? 0u : (uint32_t)min((int64_t)items_a, (int64_t)total_workers);
   bool first_static = worker < n_static;
-  uint32_t pref_idx = 0;
-  lane0_fetch_add1(p.work_counter, pref_idx, lane);
+  const uint32_t items_dyn = (uint32_t)total_items - n_static;
+  uint32_t draw = 0;           // lane 0: the counter's value, drawn for the next item
+  enum { kNone, kDrawn, kKnown };
+  int nx = kNone;              // the item after the producer's
   const uint64_t units_magic = (0x100000000ull + units - 1) / units;  // exact: items < 2^26, units <= 64
   // the item dealt ahead is described in the ring already; lane i holds the
   // block id of its page i
@@ -324,21 +345,25 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_kernel(const __grid_con
     return base + __popc(__ballot_sync(0xffffffffu, le2)) - 1;
   };
 
+  auto draw_next = [&]() {
+    nx = kDrawn;
+    if (!first_static && items_dyn > 0) lane0_fetch_add1(p.work_counter, draw, lane);
+  };
   auto fetch_ahead = [&]() {
+    nx = kKnown;
     nx_ok = false;
     uint32_t idx;
     if (first_static) {
       idx = worker;
       first_static = false;
     } else {
-      const uint32_t b = __shfl_sync(0xffffffffu, pref_idx, 0);
-      const uint32_t items_dyn = (uint32_t)total_items - n_static;
+      if (items_dyn == 0) return;
+      const uint32_t b = __shfl_sync(0xffffffffu, draw, 0);
       if (b >= items_dyn) {
         // every warp draws once past the end; the last of them resets
         if (b == items_dyn + total_workers - 1 && lane == 0) atomicExch(p.work_counter, 0u);
         return;
       }
-      lane0_fetch_add1(p.work_counter, pref_idx, lane);
       idx = n_static + b;
     }
     const uint32_t x = (uint32_t)(((uint64_t)idx * units_magic) >> 32);
@@ -379,7 +404,10 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_kernel(const __grid_con
   };
 
   auto next_item = [&]() -> bool {
+    if (nx == kNone) draw_next();
+    if (nx == kDrawn) fetch_ahead();
     if (!nx_ok) return false;
+    nx = kNone;
     __syncwarp();
     const ItemDesc d = ws.items[prod_items % kRing];
     ++prod_items;
@@ -389,9 +417,9 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_kernel(const __grid_con
     prod_end = d.page1;
     prod_withheld = withhold_next;
     blk_win = nx_blk;
-    fetch_ahead();
     return true;
   };
+  draw_next();
   fetch_ahead();
 
   // refill one stage with the producer's next pages: two of one item, or its
@@ -454,6 +482,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_kernel(const __grid_con
       }
     }
     prod_page += kPair;
+    if (nx == kNone && prod_end - prod_page <= 2 * kPair) draw_next();
+    else if (nx == kDrawn && prod_end - prod_page <= kPair) fetch_ahead();
     ++ahead;
     __syncwarp();
   };
@@ -467,7 +497,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_kernel(const __grid_con
     return count_split(p.done + (int64_t)d.r * units + d.u, d.nsplit, lane) && !aborted;
   };
   auto merge = [&](const ItemDesc& d) {
-    merge_splits<T, D>(p, d.h0, d.heads, plan_a[d.r] + plan_b[d.r], d.nsplit, d.token);
+    merge_splits<T, D>(p.part_ml, p.part_acc, p.out, Hq, d.h0, d.heads, plan_a[d.r] + plan_b[d.r], d.nsplit, d.token);
   };
   bool pending = false;     // ws.pend[pend_at]: the item of the partial not counted yet
   int pend_at = 0;
@@ -813,12 +843,10 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_kernel(const __grid_con
       const ItemDesc& d = ws.items[k % kRing];
       if (d.nsplit > 1) count(d);
     }
-    while (nx_ok) {
-      __syncwarp();
-      const ItemDesc d = ws.items[prod_items % kRing];
-      __syncwarp();
-      fetch_ahead();
+    while (next_item()) {
+      const ItemDesc d = ws.items[(prod_items - 1) % kRing];
       if (d.nsplit > 1) count(d);
+      __syncwarp();  // before a later item takes its place
     }
   }
   // beside the prefill grid before it: this grid completes only after it

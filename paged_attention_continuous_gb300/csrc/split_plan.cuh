@@ -57,7 +57,14 @@ struct PlanRows {
   int32_t step = 1;
   int32_t max_splits = 0;
   int32_t single_pages = 0;
+  int32_t single_least = 0;  // pages of an item of that one phase, at least
 };
+
+// ceil(a / b); the 64-bit division takes several times the 32-bit one's time
+__device__ __forceinline__ int64_t ceil_div(int64_t a, int64_t b) {
+  const uint64_t x = (uint64_t)(a + b - 1);
+  return ((x | (uint64_t)b) >> 32) == 0 ? (int64_t)((uint32_t)x / (uint32_t)b) : (int64_t)(x / (uint64_t)b);
+}
 
 struct SplitPlan {
   int spa, spb;  // split sizes of the two phases, in pages
@@ -72,17 +79,14 @@ __device__ __forceinline__ SplitPlan plan_splits(const PlanRows& in, int nwarps,
                                                  int32_t* plan_b, int32_t* row_len,
                                                  int32_t* row_tok) {
   __shared__ int32_t s_red[2][kMaxWarps];
-  __shared__ int32_t s_spa, s_spb, s_longest;
-  if (in.max_splits > 0) {
-    if (threadIdx.x == 0) s_longest = 0;
-    __syncthreads();
-  }
+  __shared__ int32_t s_spa, s_spb;
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
   const int nthreads = nwarps * 32;
   // Rows are checked once here and kept in shared memory; a row that fails a
   // check gets length 0 (no items) and its error bit.
   int64_t my_pages = 0;
+  int32_t my_longest = 0;
   for (int i = threadIdx.x; i < in.num_rows; i += nthreads) {
     const int r = in.row_begin + i;
     int L = in.seq_lens[r];
@@ -105,31 +109,40 @@ __device__ __forceinline__ SplitPlan plan_splits(const PlanRows& in, int nwarps,
     row_len[i] = L;
     row_tok[i] = q0;
     my_pages += pages;
-    if (in.max_splits > 0) atomicMax(&s_longest, pages);
+    my_longest = max(my_longest, pages);
   }
+  my_longest = __reduce_max_sync(0xffffffffu, my_longest);
   for (int o = 16; o > 0; o >>= 1) my_pages += __shfl_xor_sync(0xffffffffu, my_pages, o);
-  if (lane == 0) s_red[0][warp] = (int32_t)(my_pages < 0x3fffffff ? my_pages : 0x3fffffff);
+  if (lane == 0) {
+    s_red[0][warp] = (int32_t)(my_pages < 0x3fffffff ? my_pages : 0x3fffffff);
+    s_red[1][warp] = my_longest;
+  }
   __syncthreads();
   if (threadIdx.x == 0) {
     int64_t tot = 0;
-    for (int w = 0; w < nwarps; ++w) tot += s_red[0][w];
+    int32_t longest = 0;
+    for (int w = 0; w < nwarps; ++w) {
+      tot += s_red[0][w];
+      longest = max(longest, s_red[1][w]);
+    }
     const int64_t units = tot * in.units;
     const int64_t units_b = units / kTailDiv;
     const int64_t workers = (int64_t)gridDim.x * nwarps;
     const int64_t items_a = in.items_a;
-    int64_t spa = (units - units_b + workers * items_a - 1) / (workers * items_a);
-    int64_t spb = (units_b + workers * kItemsB - 1) / (workers * kItemsB);
+    int64_t spa = ceil_div(units - units_b, workers * items_a);
+    int64_t spb = ceil_div(units_b, workers * kItemsB);
     if (spa < kMinSplitPages) spa = kMinSplitPages;
     if (spb < 1) spb = 1;
     if (in.max_splits > 0) {
-      const int64_t least = (s_longest + in.max_splits - 1) / in.max_splits;
+      const int64_t least = ceil_div(longest, in.max_splits);
       if (units <= workers * in.single_pages) {
-        spb = (units + workers - 1) / workers;
+        spb = ceil_div(units, workers);
+        if (spb < in.single_least) spb = in.single_least;
         if (spb < least) spb = least;
         spa = 1 << 20;
       } else {
         if (spa < least) spa = least;
-        const int64_t tail = (s_longest / kTailDiv + spa) * 2 / in.max_splits;
+        const int64_t tail = (longest / kTailDiv + spa) * 2 / in.max_splits;
         if (spb < tail) spb = tail;
       }
     }
