@@ -64,12 +64,17 @@ using namespace decode;
 constexpr int kWarps = 8;
 constexpr int kMaxHeads = 16;  // query heads of an item
 constexpr int kPair = 2;       // pages of a stage
-// An item costs a few microseconds beside its pages (its queries, its place
-// in the plan, its partial and ticket), and joining a row's splits about one
-// for 8 of them.  So a step with few pages to a warp is cut into one item
-// each (8 requests of up to 512 tokens: 13.6 us, 19 with two phases), and a
-// long row into at most 64 splits and the last phase's (one request of 32k
-// tokens: 46 us, 65 without the limit).
+// An item costs about two microseconds beside its pages (its queries, its
+// place in the plan, its partial and ticket), and joining a row's splits about
+// one for 8 of them.  So a row is cut into equal splits, of a size that gives
+// each warp kItemsEven of them (64 requests of up to 4k tokens: 64.1 us; 68.4
+// with one, 69.9 with three; 67.5 with whole multiples of one size, whose
+// remainders all went to the last phase).  A step with few pages to a warp is
+// cut into one item each, of at least kSingleLeast pages (8 requests of up to
+// 512 tokens: 12.4 us, 13.4 without the least, 19 with two phases), and a long
+// row into at most kMaxSplits and the last phase's (one request of 32k tokens:
+// 41 us; without the limit half as long again).
+constexpr int kItemsEven = 2;
 constexpr int kSinglePages = 8;
 constexpr int kSingleLeast = 4;
 constexpr int kMaxSplits = 64;
@@ -286,7 +291,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_kernel(const __grid_con
 
   const SplitPlan plan = plan_splits<kWarps>(
       PlanRows{p.seq_lens, p.cu_seqlens_q, p.row_begin, p.num_rows, p.num_tokens, W, units, win,
-               p.max_slots, p.pdl_mode == 2 ? kItemsABeside : kItemsA, p.error_word, kPair, kMaxSplits, kSinglePages, kSingleLeast},
+               p.max_slots, p.pdl_mode == 2 ? kItemsABeside : kItemsEven, p.error_word, kPair, kPair, kMaxSplits, kSinglePages, kSingleLeast},
       nwarps, plan_a, plan_b, row_len, row_tok);
   const int spa0 = plan.spa, spb0 = plan.spb;
   const int num_a = plan_a[p.num_rows];
@@ -372,16 +377,17 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_kernel(const __grid_con
     const int a0 = plan_a[i], na = plan_a[i + 1] - a0, b0 = plan_b[i], nb = plan_b[i + 1] - b0;
     const int split = phase_a ? (int)x - a0 : (int)x - num_a - b0;
     const int L = row_len[i];
-    const int fp = first_page(L, win);
+    const int fp = first_page(L, win), end = (L + kPageTokens - 1) / kPageTokens;
+    const RowSplit rs = row_split(end - fp, spa0, spb0, kPair);
     nx_ok = true;
     const int u = (int)(idx - x * (uint32_t)units);
     int page0, page1;
     if (phase_a) {
-      page0 = fp + split * spa0;
-      page1 = page0 + spa0;
+      page0 = fp + split * rs.size;
+      page1 = min(end, page0 + rs.size);
     } else {
-      page0 = fp + na * spa0 + split * spb0;
-      page1 = min((L + kPageTokens - 1) / kPageTokens, page0 + spb0);
+      page0 = fp + rs.bp + split * spb0;
+      page1 = min(end, page0 + spb0);
     }
     if (lane == 0) {
       ItemDesc& d = ws.items[prod_items % kRing];

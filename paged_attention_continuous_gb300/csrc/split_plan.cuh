@@ -24,18 +24,27 @@ constexpr int kPlanSmemBytes = (2 * (kPlanMax + 1) + 2 * kPlanMax) * (int)sizeof
 // phase B covers the rest, [bp, pages), in nb splits of spb pages (the last
 // one shorter).
 struct RowSplit {
-  int na, bp, nb;
+  int na, size, bp, nb;
 };
 
 // First key and first page a decode row of length L reads (window W, 0 = all).
 __device__ __forceinline__ int first_key(int L, int W) { return W > 0 && L > W ? L - W : 0; }
 __device__ __forceinline__ int first_page(int L, int W) { return first_key(L, W) / kPageTokens; }
 
-__device__ __forceinline__ RowSplit row_split(int pages, int spa, int spb) {
+// With `even` > 0 the leading part is cut into equal splits instead, whole
+// multiples of `even` pages and as near to spa as that comes, so that less is
+// left for phase B (the last of them may end the row, and be shorter).
+__device__ __forceinline__ RowSplit row_split(int pages, int spa, int spb, int even = 0) {
   RowSplit s;
   const int big = pages - pages / kTailDiv;
+  s.size = spa;
   s.na = big / spa;
-  s.bp = s.na * spa;
+  if (even > 0 && spa < (1 << 20) && big > 0) {
+    const int n = max(1, (big + spa / 2) / spa);
+    s.size = ((big + n - 1) / n + even - 1) / even * even;
+    s.na = (big + s.size - 1) / s.size;
+  }
+  s.bp = min(s.na * s.size, pages);
   s.nb = (pages - s.bp + spb - 1) / spb;
   return s;
 }
@@ -50,11 +59,12 @@ struct PlanRows {
   int32_t max_slots;    // partial slots available (>= 2 * num_rows)
   int32_t items_a;      // phase-A items per warp (target)
   uint32_t* error_word;
-  // Splits are whole multiples of `step` pages.  max_splits > 0: the
+  // Splits are whole multiples of `step` pages (even: see row_split).  max_splits > 0: the
   // longest row has at most that many phase-A splits, and half as many in
   // phase B; and with at most single_pages pages to a warp there is one phase,
   // of one item to a warp (and that limit).
   int32_t step = 1;
+  int32_t even = 0;
   int32_t max_splits = 0;
   int32_t single_pages = 0;
   int32_t single_least = 0;  // pages of an item of that one phase, at least
@@ -164,7 +174,7 @@ __device__ __forceinline__ SplitPlan plan_splits(const PlanRows& in, int nwarps,
     for (int i = b; i < e; ++i) {
       const int Li = row_len[i];
       const RowSplit rs =
-          row_split((Li + kPageTokens - 1) / kPageTokens - first_page(Li, in.window), spa0, spb0);
+          row_split((Li + kPageTokens - 1) / kPageTokens - first_page(Li, in.window), spa0, spb0, in.even);
       const int na = rs.na, nb = rs.nb;
       plan_a[i + 1] = na;
       plan_b[i + 1] = nb;
