@@ -117,6 +117,7 @@ struct Bars {
   // is queued only after their softmax of tile j + 1.
   alignas(16) float scales[kScaleSlots][kPages][4];
   int32_t nan_first[128], nan_last[128];  // by dim: keys whose value is NaN
+  int32_t nan_any;
 };
 
 template <int D>
@@ -311,6 +312,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       for (int w = 0; w < 4; ++w) mbar_init(&B->turn[t][w], 1);
     }
     B->abort = 0;
+    B->nan_any = 0;
     B->seq_len = L;
     B->n_tiles = n_tiles;
     B->npages = npages;
@@ -449,6 +451,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
 #pragma unroll
           for (int b = 0; b < 4; ++b) x[b] = row < end ? w[i][b] : 0u;
           if (nan_codes(x[0]) | nan_codes(x[1]) | nan_codes(x[2]) | nan_codes(x[3])) {
+            *reinterpret_cast<volatile int32_t*>(&B->nan_any) = 1;
 #pragma unroll
             for (int b = 0; b < 16; ++b)
               if (((x[b >> 2] >> (8 * (b & 3))) & 0x7fu) == 0x7fu) {
@@ -567,47 +570,68 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     const int row = threadIdx.x & 127;            // == TMEM lane
     const int tl = row / G;
     const int tok = tok0 + t * tpt + tl;
-    const int head = g * G + (row - tl * G);
     const bool valid = t < kTiles && tl < tpt && tok < q_len;
     const int pos = start + (valid ? tok : q_len - 1);
+    // A warp copies its 32 rows of q and out kRowsAtOnce at a time, a row's
+    // 16-byte chunks in neighbouring lanes, and turns them in shared memory: a
+    // thread that reads or writes a row of its own touches a line for every
+    // chunk (Q took 6 us of a CTA and O 8, now 3.5 and 3).
+    constexpr int N = rope::Vec<T>::kN;
+    constexpr int kChunks = D / N;
+    constexpr int kRowsAtOnce = 32 / kChunks;
+    const int chunk = lane % kChunks, sub = lane / kChunks;
+    const uint32_t by_g = (65536u + G - 1) / G;   // x / G = x by_g / 2^16 for x < 128
+    const int64_t first = ((int64_t)(q0 + tok0 + t * tpt) * p.num_q_heads + g * G) * D + chunk * N;
+    // elements of q (and out) before the lane's chunk of row rr of the tile, or -1
+    auto row_at = [&](int rr) -> int64_t {
+      const int rt = (int)((uint32_t)rr * by_g >> 16);
+      if (rt >= tpt || tok0 + t * tpt + rt >= q_len) return -1;
+      return first + (int64_t)(rt * p.num_q_heads + rr - rt * G) * D;
+    };
     float hs = 1.f;                               // score factor of the row
     if (t < kTiles) {
-      // Q row -> halves in shared memory, the largest magnitude at [2^14,
-      // 2^15); the scale's sign goes with Q, and a scale of 0 makes Q zero
-      const T* src = static_cast<const T*>(p.q) + ((int64_t)(q0 + (valid ? tok : q_len - 1)) * p.num_q_heads +
-                                                   (valid ? head : g * G)) * D;
-      float amax = 0.f;
-      if (valid) {
+      // Q rows -> halves in shared memory, the largest magnitude at [2^14,
+      // 2^15); the scale's sign goes with Q, and a scale of 0 makes Q zero.
+      // First as they are: chunk c of a row where its halves will be (float32:
+      // chunks from 16 on in the place of the low halves).
+      uint8_t* qs = smem + Smem<D>::q + t * kTile;
+      auto raw_at = [&](int rr, int c) {
+        constexpr int kPer = D / 8;
+        return qs + (c >= kPer ? kTile : 0u) + ((c % kPer) >> 3) * kHalf + swz(rr, c & 7);
+      };
 #pragma unroll 4
-        for (int i = 0; i < D / 8; ++i) {
-          float x[8];
-          if constexpr (kF32) {
-            rope::Vec<float>::load(__ldg(reinterpret_cast<const uint4*>(src) + 2 * i), x);
-            rope::Vec<float>::load(__ldg(reinterpret_cast<const uint4*>(src) + 2 * i + 1), x + 4);
-          } else {
-            rope::Vec<__nv_bfloat16>::load(__ldg(reinterpret_cast<const uint4*>(src) + i), x);
-          }
+      for (int i = 0; i < kChunks; ++i) {
+        const int rr = (warp & 3) * 32 + i * kRowsAtOnce + sub;
+        const int64_t at = row_at(rr);
+        // (0 bytes: zeros)
+        cp_async16(smem_addr(raw_at(rr, chunk)), static_cast<const T*>(p.q) + max(at, (int64_t)0), at >= 0 ? 16 : 0);
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
+      __syncwarp();
+      uint4 raw[kChunks];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(x[e]));
-        }
+      for (int i = 0; i < kChunks; ++i) raw[i] = *reinterpret_cast<const uint4*>(raw_at(row, i));
+      auto load8 = [&](int i, float* x) {
+        rope::Vec<T>::load(raw[i * (8 / N)], x);
+        if constexpr (N == 4) rope::Vec<T>::load(raw[2 * i + 1], x + 4);
+      };
+      float amax = 0.f;
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) {
+        float x[8];
+        load8(i, x);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(x[e]));
       }
       // zeros, or a row that is not finite (nor are its scores): factor 1
       const int k = amax > 0.f && amax <= 3.402823466e38f ? max((int)(__float_as_uint(amax) >> 23) - 127, -110) : 14;
       const float up = p.scale_log2 == 0.f ? 0.f : p.scale_log2 < 0.f ? -q8::exp2i(14 - k) : q8::exp2i(14 - k);
       // (never so small that times a block's scale it is 0: a masked score is -inf)
       hs = p.scale_log2 == 0.f ? 1.f : fmaxf(fabsf(p.scale_log2) * q8::exp2i(k - 14), q8::exp2i(-80));
-      uint8_t* qs = smem + Smem<D>::q + t * kTile;
-#pragma unroll 4
+#pragma unroll
       for (int i = 0; i < D / 8; ++i) {
-        float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        if (valid) {
-          if constexpr (kF32) {
-            rope::Vec<float>::load(__ldg(reinterpret_cast<const uint4*>(src) + 2 * i), x);
-            rope::Vec<float>::load(__ldg(reinterpret_cast<const uint4*>(src) + 2 * i + 1), x + 4);
-          } else {
-            rope::Vec<__nv_bfloat16>::load(__ldg(reinterpret_cast<const uint4*>(src) + i), x);
-          }
-        }
+        float x[8];
+        load8(i, x);
         uint32_t h[4], lo[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -776,7 +800,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       if (w) {
         tc::fence_after_sync();
         const float inv = 1.f / l_run;
-        T* dst = static_cast<T*>(p.out) + ((int64_t)(q0 + tok) * p.num_q_heads + head) * D;
+        // The rows are turned in shared memory, so that a warp stores whole
+        // ones: Q's place is free (its last product preceded O's).
+        uint8_t* turn = smem + Smem<D>::q + t * kTile + (warp & 3) * (32 * kChunks * 16);
+        const bool any_nan = *reinterpret_cast<volatile int32_t*>(&B->nan_any) != 0;
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
           float o[32];
@@ -787,18 +814,28 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
 #pragma unroll
             for (int e = 0; e < 32; ++e) o[e] += a[e];
           }
-          if (valid) {
+#pragma unroll
+          for (int e = 0; e < 32; ++e) o[e] *= inv;
+          if (any_nan) {
 #pragma unroll
             for (int e = 0; e < 32; ++e) {
-              o[e] *= inv;
               const int a = B->nan_first[32 * c + e], b = B->nan_last[32 * c + e];
               if ((a <= pos && a >= key_row) || (b >= 0 && b <= pos && b >= key_row)) o[e] = __int_as_float(0x7fffffff);
             }
-            constexpr int N = rope::Vec<T>::kN;
-#pragma unroll
-            for (int e = 0; e < 32; e += N)
-              reinterpret_cast<uint4*>(dst)[(32 * c + e) / N] = rope::Vec<T>::store(o + e);
           }
+#pragma unroll
+          for (int e = 0; e < 32; e += N) {
+            const int at = (32 * c + e) / N;
+            *reinterpret_cast<uint4*>(turn + (lane * kChunks + (at ^ (lane & 7))) * 16) = rope::Vec<T>::store(o + e);
+          }
+        }
+        __syncwarp();
+#pragma unroll 4
+        for (int i = 0; i < kChunks; ++i) {
+          const int rr = i * kRowsAtOnce + sub;       // of the warp's rows
+          const uint4 v = *reinterpret_cast<const uint4*>(turn + (rr * kChunks + (chunk ^ (rr & 7))) * 16);
+          const int64_t at = row_at((warp & 3) * 32 + rr);
+          if (at >= 0) *reinterpret_cast<uint4*>(static_cast<T*>(p.out) + at) = v;
         }
       }
     }
