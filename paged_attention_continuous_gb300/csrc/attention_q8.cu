@@ -152,16 +152,25 @@ extern "C" cb_status cb_paged_attention_q8(const cb_attention_args* args, const 
   using cb::decode::After;
   uint32_t* ew = static_cast<uint32_t*>(a.workspace);
   const int nd = a.num_decodes;
+  // Splits of few prefill rows leave their parts in the last places of the
+  // workspace, at most half of them; the decodes' are the ones before.
+  const cb::WsLayout L = cb::ws_layout(a.num_reqs, a.num_q_heads, a.num_kv_heads, a.head_dim);
+  cb::decode::Scratch scratch = cb::decode_scratch(a, L);
+  cb::prefill_q8::Parts parts{cb::prefill_q8::splits(a, L.slots / 2), nullptr, nullptr};
+  if (parts.splits > 1) {
+    scratch.slots -= (int64_t)a.num_tokens * parts.splits;
+    parts.ml = scratch.part_ml + scratch.slots * a.num_q_heads * 2;
+    parts.acc = scratch.part_acc + scratch.slots * a.num_q_heads * a.head_dim;
+  }
   auto run_decode = [&](After after) {
-    const cb::WsLayout L = cb::ws_layout(a.num_reqs, a.num_q_heads, a.num_kv_heads, a.head_dim);
-    return cb::decode_q8::dispatch(a, k_scales, v_scales, scale_stride, cb::decode_scratch(a, L), ew, stream, after);
+    return cb::decode_q8::dispatch(a, k_scales, v_scales, scale_stride, scratch, ew, stream, after);
   };
   auto run_prefill = [&](bool overlap) {
-    return cb::prefill_q8::launch(a, k_scales, v_scales, scale_stride, ew, stream, overlap);
+    return cb::prefill_q8::launch(a, k_scales, v_scales, scale_stride, parts, ew, stream, overlap);
   };
   bool decodes_left = nd > 0, prefills_left = nd < a.num_reqs;
   const int64_t ctas = cb::prefill_q8::ctas(a);
-  if (decodes_left && ctas > 0 && a.max_seq_len >= 16384 && ctas + 16 <= cb::sm_count_current_device()) {
+  if (decodes_left && ctas > 0 && parts.splits == 1 && a.max_seq_len >= 16384 && ctas + 16 <= cb::sm_count_current_device()) {
     st = run_prefill(false);
     if (st != CB_OK && st != CB_ERR_UNSUPPORTED) return st;
     if (st == CB_OK) {

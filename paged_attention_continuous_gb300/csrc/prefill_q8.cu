@@ -39,12 +39,27 @@
 //     of floats, the reference a whole number near the largest exponent.  The
 //     tensor core drops bits wherever it adds to a large accumulator, so each
 //     tile's P.V starts from zero and the softmax warps add it to the output
-//     (at 1000 keys the error is that of float32 torch then, and 2 to 3
-//     times that with one accumulator).
+//     (largest error at 1000 keys 0.6 to 1.1e-6; 0.9 to 1.7e-6 with one
+//     accumulator, 0.4 to 0.9e-6 for a plain float32 form).
 //   * A value code that is NaN must not reach rows that do not see its key
 //     (weight 0 times NaN is NaN): in tiles that some row of the CTA sees only
 //     in part, converters store such codes as 0 and note the first and last
 //     key for each dim; the epilogue writes NaN where a row sees one.
+//
+//   * Few rows with many keys would leave most SMs idle: when the CTAs fill
+//     less than half of them, each one's KV tiles are split over as many CTAs
+//     as there are SMs for (at least four tiles each), which leave float32
+//     parts that a second kernel joins (64 tokens of 64 heads behind 16k: 61
+//     us, 265 without; 16 tokens of 32 heads behind 100k: 169 and 1344; 64 of
+//     32 behind 2k: 26 and 44; 64 behind 900, under eight tiles: not split).
+//
+// What bounds it: the chain of a KV tile, 2.0 us for 128 keys and both query
+// tiles.  Its products are 1.1 us of tensor core time, its 32k exponentials
+// 0.55 us of the four exponential units each, and shared memory moves codes,
+// halves and operands for 1.3 us; the rest is the turns that the two query
+// tiles' softmax take with them.  512 tokens of 64 heads behind 16k (128
+// CTAs of 152 SMs): 277 us, 1.0 PFLOP/s, 54% of the measured bfloat16 rate;
+// a CTA costs 7 us beside its tiles.
 //
 // Tensor memory: S0 | S1 | O0 | O1 at columns 0, 128, 256, 384; P_t is
 // written over S_t as half pairs and read from there as the A operand.
@@ -60,6 +75,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <atomic>
 #include <type_traits>
 
@@ -88,6 +104,10 @@ constexpr int kThreads = 512;
 constexpr int kRegsSoftmax = 192, kRegsMma = 48, kRegsConv = 80;
 static_assert(128 * (2 * kRegsSoftmax + kRegsMma + kRegsConv) <= 65536, "register split");
 constexpr uint32_t kHalf = 128 * 128;  // 128 rows of 64 halves
+// A CTA costs about 7 us beside its KV tiles, of 2 us each, so a split of the
+// keys has at least four of them.
+constexpr int kLeastTiles = 4;
+constexpr int kMaxSplits = 16;
 constexpr uint32_t kTmemCols = 512;
 // weight exponent at the reference, which moves when passed by more than the
 // lag (float32: exponents near 0 are the most exact)
@@ -111,7 +131,7 @@ struct Bars {
   int32_t row, pair;
   // what the CTA works on; the roles read it where they need it (kept in
   // registers from the prologue on, it would spill)
-  int32_t seq_len, n_tiles, npages, lo_pg, first_pos, last_pos, table_row;
+  int32_t seq_len, n_tiles, npages, lo_pg, first_pos, last_pos, table_row, split;
   // Of each block of recent KV tiles: 2^ek, ev, 2^-ev.  The slot of tile j is rewritten for tile j +
   // 4, which is expanded only after Q.K(j + 2) of both query tiles, and that
   // is queued only after their softmax of tile j + 1.
@@ -151,6 +171,11 @@ struct Params {
   float scale_log2_low;       // what float32 leaves of it, as a share of it
   int32_t window;
   uint32_t* error_word;
+  // splits of the keys of a (row, pair of query tiles); with more than one,
+  // token i of the prefill rows leaves split s's part at slot i * splits + s
+  int32_t splits;
+  float* part_ml;             // [slots][Hq][2]: reference and sum of weights
+  float* part_acc;            // [slots][Hq][D]
   uint64_t wait_ns;
   int32_t withhold_tile;      // test hook: CTA 0 never copies this raw K tile (-1: none)
 };
@@ -203,6 +228,32 @@ __device__ __forceinline__ uint32_t nan_codes(uint32_t w) {
   return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
 }
 
+// A row's tokens and length lie within the call's (and its parts' places).
+__device__ __forceinline__ bool row_fits(const Params& p, int q0, int q_len, int L) {
+  const int first = p.splits > 1 ? p.cu_seqlens_q[p.row_begin] : 0;
+  return first >= 0 && q0 >= first && q_len <= p.num_tokens - q0 && L >= q_len &&
+         (L - 1) / kPage < p.max_blocks_per_seq;
+}
+
+// The KV tiles of a (row, pair of query tiles) and of each of its splits.
+struct Tiles {
+  int key_lo;         // with a window, the first key that the first query sees
+  int first, last;    // tiles [first, last)
+  int of_split;       // tiles of a split; the last one may have fewer
+  int splits;         // that have any
+};
+// start: cached tokens of the row; [tok0, tok0 + tpp) the pair's tokens
+__device__ __forceinline__ Tiles tiles_of(const Params& p, int start, int q_len, int tok0, int tpp) {
+  Tiles t;
+  t.key_lo = p.window > 0 ? max(0, start + tok0 - p.window + 1) : 0;
+  t.first = t.key_lo / kBN;
+  t.last = (start + min(tok0 + tpp - 1, q_len - 1)) / kBN + 1;
+  const int n = t.last - t.first;
+  t.of_split = p.splits > 1 ? max((n + p.splits - 1) / p.splits, kLeastTiles) : n;
+  t.splits = p.splits > 1 ? (n + t.of_split - 1) / t.of_split : 1;
+  return t;
+}
+
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_constant__ Params p) {
   constexpr bool kF32 = std::is_same<T, float>::value;
@@ -222,12 +273,15 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
   const int tpt = kBM / G;                        // tokens per query tile
   const int tpp = kTiles * tpt;                   // of a CTA
   const int Hkv = p.num_kv_heads;
-  const int g = (int)(blockIdx.x % (unsigned)Hkv);
+  const unsigned units = gridDim.x / (unsigned)p.splits;     // (row, pair, KV head)s
+  const int split = (int)(blockIdx.x / units);
+  const unsigned unit = blockIdx.x - split * units;
+  const int g = (int)(unit % (unsigned)Hkv);
   // ---- which (row, pair) this CTA serves: warp 0 scans the rows' pair
   // counts; every row's latest (heaviest) pair comes first
   if (warp == 0) {
-    const int x = (int)(blockIdx.x / (unsigned)Hkv);
-    const int num_pairs = (int)(gridDim.x / (unsigned)Hkv);
+    const int x = (int)(unit / (unsigned)Hkv);
+    const int num_pairs = (int)(units / (unsigned)Hkv);
     int run = 0, row = -1, pair = 0;
     bool bad = false;
     for (int b = 0; b < p.num_rows; b += 32) {
@@ -273,9 +327,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
   const int q0 = p.cu_seqlens_q[r];
   const int q_len = p.cu_seqlens_q[r + 1] - q0;
   const int L = p.seq_lens[r];
-  const int W = p.max_blocks_per_seq;
-  if (q0 < 0 || q0 + q_len > p.num_tokens || L < q_len || (L + kPage - 1) / kPage > W) {
-    if (threadIdx.x == 0 && mp == 0 && g == 0) set_error(p.error_word, CB_DEVERR_SEQ_RANGE);
+  if (!row_fits(p, q0, q_len, L)) {
+    if (threadIdx.x == 0 && mp == 0 && g == 0 && split == 0) set_error(p.error_word, CB_DEVERR_SEQ_RANGE);
     order_after_previous_grid();
     return;
   }
@@ -283,12 +336,15 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
   const bool has_t1 = kTiles == 2 && tok0 + tpt < q_len;
   const int start = L - q_len;
   const int last_tok = min(tok0 + tpp - 1, q_len - 1);
-  const int n_tiles = (start + last_tok) / kBN + 1;
   const int npages = (L + kPage - 1) / kPage;
-  // with a window, the first query reads keys from key_lo on: KV tiles j_lo ..
-  const int key_lo = p.window > 0 ? max(0, start + tok0 - p.window + 1) : 0;
-  const int j_lo = key_lo / kBN;
-  const int lo_pg = key_lo / kPage;
+  const Tiles tiles = tiles_of(p, start, q_len, tok0, tpp);
+  if (split >= tiles.splits) {
+    order_after_previous_grid();
+    return;
+  }
+  const int lo_pg = tiles.key_lo / kPage;
+  const int j_lo = tiles.first + split * tiles.of_split;
+  const int n_tiles = min(tiles.last, j_lo + tiles.of_split);
   const int nt = n_tiles - j_lo;
 
   if ((warp == 8 || warp == 9) && lane == 0) tc::prefetch_tensormap(warp == 8 ? &p.tmap_k : &p.tmap_v);
@@ -320,6 +376,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     B->first_pos = start + tok0;
     B->last_pos = start + last_tok;
     B->table_row = r;
+    B->split = tiles.splits > 1 ? split : -1;
     fence_barrier_init();
   }
   if (threadIdx.x < 128) {
@@ -799,10 +856,34 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       if (!w) abort_cta(B, p.error_word);
       if (w) {
         tc::fence_after_sync();
-        const float inv = 1.f / l_run;
+        const int part = VB->split;                 // -1: the row's only one
+        const bool parted = part >= 0;
+        const float inv = parted ? 1.f : 1.f / l_run;
         // The rows are turned in shared memory, so that a warp stores whole
         // ones: Q's place is free (its last product preceded O's).
         uint8_t* turn = smem + Smem<D>::q + t * kTile + (warp & 3) * (32 * kChunks * 16);
+        auto slot_of = [&](int rr) -> int64_t {
+          const int rt = (int)((uint32_t)rr * by_g >> 16);
+          if (rt >= tpt || tok0 + t * tpt + rt >= q_len) return -1;
+          return (int64_t)(q0 - p.cu_seqlens_q[p.row_begin] + tok0 + t * tpt + rt) * p.splits + part;
+        };
+        auto head_of = [&](int rr) { return g * G + rr - (int)((uint32_t)rr * by_g >> 16) * G; };
+        auto store_part = [&](uint8_t* turn, int c, const float* o) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            *reinterpret_cast<float4*>(turn + (lane * 8 + (e ^ (lane & 7))) * 16) =
+                make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+          __syncwarp();
+#pragma unroll 2
+          for (int i = 0; i < 8; ++i) {
+            const int rr = i * 4 + lane / 8;          // of the warp's rows
+            const float4 v = *reinterpret_cast<const float4*>(turn + (rr * 8 + (lane % 8 ^ (rr & 7))) * 16);
+            const int64_t slot = slot_of((warp & 3) * 32 + rr);
+            if (slot >= 0)
+              reinterpret_cast<float4*>(p.part_acc + (slot * p.num_q_heads + head_of((warp & 3) * 32 + rr)) * D + 32 * c)[lane % 8] = v;
+          }
+          __syncwarp();  // before the next dims take its place
+        };
         const bool any_nan = *reinterpret_cast<volatile int32_t*>(&B->nan_any) != 0;
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
@@ -823,6 +904,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
               if ((a <= pos && a >= key_row) || (b >= 0 && b <= pos && b >= key_row)) o[e] = __int_as_float(0x7fffffff);
             }
           }
+          if (parted) {
+            // 32 dims of this split's part, in float32, row by row
+            store_part(turn, c, o);
+            continue;
+          }
 #pragma unroll
           for (int e = 0; e < 32; e += N) {
             const int at = (32 * c + e) / N;
@@ -830,8 +916,12 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
           }
         }
         __syncwarp();
+        if (parted) {
+          const int64_t slot = slot_of(row);
+          if (slot >= 0) *reinterpret_cast<float2*>(p.part_ml + (slot * p.num_q_heads + head_of(row)) * 2) = make_float2(m_run, l_run);
+        }
 #pragma unroll 4
-        for (int i = 0; i < kChunks; ++i) {
+        for (int i = 0; i < kChunks && !parted; ++i) {
           const int rr = i * kRowsAtOnce + sub;       // of the warp's rows
           const uint4 v = *reinterpret_cast<const uint4*>(turn + (rr * kChunks + (chunk ^ (rr & 7))) * 16);
           const int64_t at = row_at((warp & 3) * 32 + rr);
@@ -847,17 +937,79 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
   order_after_previous_grid();
 }
 
+// Joins the splits' parts of the prefill rows' outputs: one warp for each
+// (token, head); sum_s 2^(m_s - M) acc_s / sum_s 2^(m_s - M) l_s, in the
+// splits' order.  Bound by its latency (a search for the token's row, then
+// all parts at once).
+template <typename T, int D>
+__global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Params p) {
+  constexpr bool kF32 = std::is_same<T, float>::value;
+  constexpr int kE = D / 32;                      // elements of a lane
+  const int lane = threadIdx.x & 31;
+  const int64_t w = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int i = (int)(w / p.num_q_heads), head = (int)(w - (int64_t)i * p.num_q_heads);
+  const int32_t* cu = p.cu_seqlens_q + p.row_begin;
+  const int token = cu[0] + i;
+  if (cu[0] < 0 || token >= cu[p.num_rows] || token >= p.num_tokens) return;
+  int lo = 0, hi = p.num_rows - 1;                // the row with cu[row] <= token < cu[row + 1]
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (cu[mid] <= token) lo = mid; else hi = mid - 1;
+  }
+  const int q_len = cu[lo + 1] - cu[lo], L = p.seq_lens[p.row_begin + lo];
+  if (token < cu[lo] || token >= cu[lo + 1] || !row_fits(p, cu[lo], q_len, L)) return;
+  const int tpp = (kF32 ? 1 : 2) * (kBM / p.group);
+  const int tok0 = (token - cu[lo]) / tpp * tpp;
+  const Tiles t = tiles_of(p, L - q_len, q_len, tok0, tpp);
+  if (t.splits <= 1) return;                      // the CTA has written its rows
+  const int64_t first = (int64_t)i * p.splits;
+  float2 ml = make_float2(-INFINITY, 0.f);
+  if (lane < t.splits) ml = reinterpret_cast<const float2*>(p.part_ml)[(first + lane) * p.num_q_heads + head];
+  float acc[kMaxSplits][kE];
+#pragma unroll
+  for (int s = 0; s < kMaxSplits; ++s) {
+    const float* part = p.part_acc + ((first + s) * p.num_q_heads + head) * D + kE * lane;
+#pragma unroll
+    for (int e = 0; e < kE; e += 2) {
+      const float2 v = s < t.splits ? *reinterpret_cast<const float2*>(part + e) : make_float2(0.f, 0.f);
+      acc[s][e] = v.x;
+      acc[s][e + 1] = v.y;
+    }
+  }
+  float M = ml.x;
+#pragma unroll
+  for (int o = kMaxSplits / 2; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+  M = __shfl_sync(0xffffffffu, M, 0);
+  const float weight = lane < t.splits ? exp2f(ml.x - M) : 0.f;
+  float l = weight * ml.y, out[kE] = {};
+#pragma unroll
+  for (int o = kMaxSplits / 2; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+  l = __shfl_sync(0xffffffffu, l, 0);
+#pragma unroll
+  for (int s = 0; s < kMaxSplits; ++s) {
+    const float f = __shfl_sync(0xffffffffu, weight, s);
+    if (s < t.splits) {
+#pragma unroll
+      for (int e = 0; e < kE; ++e) out[e] = fmaf(f, acc[s][e], out[e]);
+    }
+  }
+  T* dst = static_cast<T*>(p.out) + ((int64_t)token * p.num_q_heads + head) * D + kE * lane;
+  const float inv = 1.f / l;
+#pragma unroll
+  for (int e = 0; e < kE; e += 2) decode::store2(dst + e, out[e] * inv, out[e + 1] * inv);
+}
+
 namespace {
 
 template <typename T, int D>
 cb_status launch_kernel(const cb_attention_args& a, const uint8_t* k_scales, const uint8_t* v_scales,
-                        int64_t scale_stride, uint32_t* error_word, cudaStream_t stream,
-                        bool overlap_previous) {
+                        int64_t scale_stride, const Parts& parts, uint32_t* error_word,
+                        cudaStream_t stream, bool overlap_previous) {
   auto kern = prefill_kernel<T, D>;
   static std::atomic<uint8_t> attr_set[kMaxDevices];
   cb_status st = ensure_smem_attr(reinterpret_cast<const void*>(kern), Smem<D>::total, attr_set);
   if (st != CB_OK) return st;
-  const int64_t n = ctas(a);
+  const int64_t n = ctas(a) * parts.splits;
   if (n <= 0) return CB_OK;
   if (n >= ((int64_t)1 << 31)) return CB_ERR_UNSUPPORTED;
   const int64_t rows = (int64_t)a.num_blocks * a.num_kv_heads * kPage;
@@ -887,6 +1039,9 @@ cb_status launch_kernel(const cb_attention_args& a, const uint8_t* k_scales, con
   p.scale_log2 = (float)scale_log2;
   p.scale_log2_low = p.scale_log2 != 0.f ? (float)((scale_log2 - p.scale_log2) / p.scale_log2) : 0.f;
   p.window = a.sliding_window;
+  p.splits = parts.splits;
+  p.part_ml = parts.ml;
+  p.part_acc = parts.acc;
   p.error_word = error_word;
   p.wait_ns = wait_limit_ns();
   p.withhold_tile = withheld_prefill_tile();
@@ -902,6 +1057,11 @@ cb_status launch_kernel(const cb_attention_args& a, const uint8_t* k_scales, con
   cfg.numAttrs = 1;
   cudaError_t e = cudaLaunchKernelEx(&cfg, kern, p);
   if (e == cudaSuccess) e = cudaGetLastError();
+  if (e == cudaSuccess && parts.splits > 1) {
+    const int64_t warps = (int64_t)a.num_tokens * a.num_q_heads;
+    join_kernel<T, D><<<(unsigned)((warps + 7) / 8), 256, 0, stream>>>(p);
+    e = cudaGetLastError();
+  }
   if (e != cudaSuccess) return fail(CB_ERR_CUDA, "prefill kernel launch: %s", cudaGetErrorString(e));
   return CB_OK;
 }
@@ -918,12 +1078,25 @@ int64_t ctas(const cb_attention_args& a) {
   return pairs * a.num_kv_heads;
 }
 
+int splits(const cb_attention_args& a, int64_t slots) {
+  const int64_t n = ctas(a);
+  if (n <= 0) return 1;
+  // keys that a pair of query tiles may see
+  int64_t keys = a.max_seq_len;
+  if (a.sliding_window > 0) keys = std::min<int64_t>(keys, (int64_t)a.sliding_window + 2 * kBM);
+  int64_t s = sm_count_current_device() / n;
+  s = std::min<int64_t>(s, kMaxSplits);
+  s = std::min<int64_t>(s, keys / (kBN * kLeastTiles));
+  s = std::min<int64_t>(s, slots / a.num_tokens);
+  return s < 2 ? 1 : (int)s;
+}
+
 cb_status launch(const cb_attention_args& a, const uint8_t* k_scales, const uint8_t* v_scales,
-                 int64_t scale_stride, uint32_t* error_word, cudaStream_t stream,
+                 int64_t scale_stride, const Parts& parts, uint32_t* error_word, cudaStream_t stream,
                  bool overlap_previous) {
   if (a.num_q_heads / a.num_kv_heads > kBM) return CB_ERR_UNSUPPORTED;
 #define CB_PRE(T, DD) \
-  return launch_kernel<T, DD>(a, k_scales, v_scales, scale_stride, error_word, stream, overlap_previous)
+  return launch_kernel<T, DD>(a, k_scales, v_scales, scale_stride, parts, error_word, stream, overlap_previous)
   if (a.dtype == CB_DTYPE_F32) {
     if (a.head_dim == 64) CB_PRE(float, 64);
     CB_PRE(float, 128);

@@ -13,12 +13,24 @@ namespace prefill_q8 {
 // where this kernel does not take them).
 int64_t ctas(const cb_attention_args& a);
 
+// Splits of each CTA's keys, 1 for none: as many as idle SMs take when the
+// CTAs fill less than half of them.  slots: places for parts, of which a call
+// with splits uses splits for each of its tokens.
+int splits(const cb_attention_args& a, int64_t slots);
+
+// Where the splits leave their parts: ml [slots][Hq][2], acc [slots][Hq][D].
+struct Parts {
+  int32_t splits;
+  float* ml;
+  float* acc;
+};
+
 // Rows [num_decodes, num_reqs) of `a`.  Returns CB_ERR_UNSUPPORTED (without a
 // message) for more than 128 query heads to a KV head.  overlap_previous: the
 // kernel queued just before on `stream` is the decode kernel of the same
 // call, which this grid may overlap (programmatic stream serialization).
 cb_status launch(const cb_attention_args& a, const uint8_t* k_scales, const uint8_t* v_scales,
-                 int64_t scale_stride, uint32_t* error_word, cudaStream_t stream,
+                 int64_t scale_stride, const Parts& parts, uint32_t* error_word, cudaStream_t stream,
                  bool overlap_previous);
 
 }  // namespace prefill_q8
