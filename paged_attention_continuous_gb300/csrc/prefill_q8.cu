@@ -54,7 +54,7 @@
 //     32 behind 2k: 26 and 44; 64 behind 900, under eight tiles: not split).
 //
 // What bounds it: the chain of a KV tile, 2.0 us for 128 keys and both query
-// tiles.  Its products are 1.1 us of tensor core time, its 32k exponentials
+// tiles.  Its products are 1.4 us at the measured matrix rate, its 32k exponentials
 // 0.55 us of the four exponential units each, and shared memory moves codes,
 // halves and operands for 1.3 us; the rest is the turns that the two query
 // tiles' softmax take with them.  512 tokens of 64 heads behind 16k (128
