@@ -70,6 +70,16 @@ def test_few_rows_and_many_keys(rows, nd, hq, hkv, D, window, dtype):
     assert c.ws.read_errors() == 0
 
 
+@pytest.mark.parametrize("rows,nd,hq,hkv,D", [
+    ([(40000, 1), (33, 1), (0, 0), (2100, 1)], 4, 8, 1, 64),            # as many splits as a row may have
+    ([(20000, 1), (17000, 1), (700, 600), (90, 17)], 2, 32, 8, 64),     # decodes beside the chunks
+])
+def test_very_long_rows(rows, nd, hq, hkv, D):
+    c = Case(rows, nd, hq, hkv, D, "bf16", seed=36, extra_tokens=1)
+    c.check(c.run())
+    assert c.ws.read_errors() == 0
+
+
 def test_parts_and_decode_parts_share_a_workspace():
     """A workspace of few rows, whose places decode and chunk rows divide, and
     graphs of it replayed in turn."""
