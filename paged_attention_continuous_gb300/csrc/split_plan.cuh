@@ -59,10 +59,10 @@ struct PlanRows {
   int32_t max_slots;    // partial slots available (>= 2 * num_rows)
   int32_t items_a;      // phase-A items per warp (target)
   uint32_t* error_word;
-  // Splits are whole multiples of `step` pages (even: see row_split).  max_splits > 0: the
-  // longest row has at most that many phase-A splits, and half as many in
-  // phase B; and with at most single_pages pages to a warp there is one phase,
-  // of one item to a warp (and that limit).
+  // Splits are whole multiples of `step` pages (even: see row_split).
+  // max_splits > 0: the longest row has about that many phase-A splits at
+  // most, and half as many in phase B; and with at most single_pages pages to
+  // a warp there is one phase, of one item to a warp (and that limit).
   int32_t step = 1;
   int32_t even = 0;
   int32_t max_splits = 0;
