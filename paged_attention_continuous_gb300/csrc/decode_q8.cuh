@@ -291,7 +291,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_kernel(const __grid_con
 
   const SplitPlan plan = plan_splits<kWarps>(
       PlanRows{p.seq_lens, p.cu_seqlens_q, p.row_begin, p.num_rows, p.num_tokens, W, units, win,
-               p.max_slots, p.pdl_mode == 2 ? kItemsABeside : kItemsEven, p.error_word, kPair, kPair, kMaxSplits, kSinglePages, kSingleLeast},
+               p.max_slots, kItemsEven, p.error_word, kPair, kPair, kMaxSplits, kSinglePages, kSingleLeast},
       nwarps, plan_a, plan_b, row_len, row_tok);
   const int spa0 = plan.spa, spb0 = plan.spb;
   const int num_a = plan_a[p.num_rows];
@@ -509,9 +509,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_kernel(const __grid_con
   int pend_at = 0;
 
   // the cache is read from here on: behind this step's append when the
-  // launch overlaps it; only then may the prefill rows of the call start
+  // launch overlaps it (a prefill grid beside has begun behind the append)
   if (p.pdl_mode != 2) asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 #pragma unroll 1
   for (int s = 0; s < kStages; ++s) produce(s);
 

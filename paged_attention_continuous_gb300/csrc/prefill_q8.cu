@@ -219,10 +219,6 @@ __device__ __forceinline__ float4 lds_float4(uint32_t addr) {
 __device__ __forceinline__ float exponent(float s, float f, float fl, float base) {
   return fmaf(fmaxf(s, -4294967296.f), fl, fmaf(s, f, base));
 }
-__device__ __forceinline__ void order_after_previous_grid() {
-  if (blockIdx.x == 0 && threadIdx.x == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
-}
-
 // Any e4m3 NaN (0x7f or 0xff) among four codes.
 __device__ __forceinline__ uint32_t nan_codes(uint32_t w) {
   return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
@@ -265,8 +261,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
   Bars* B = reinterpret_cast<Bars*>(smem + Smem<D>::bars);
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  // the decode rows of the same call, when launched after this grid with
-  // programmatic serialization, may start at once on the SMs it leaves idle
+  // the decode rows of the same call, launched after this grid with
+  // programmatic serialization, may start on the SMs that it leaves
   if (threadIdx.x == 0) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   const int G = p.group;
@@ -318,10 +314,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     }
   }
   __syncthreads();
-  if (B->row < 0) {                               // past the last pair
-    order_after_previous_grid();
-    return;
-  }
+  if (B->row < 0) return;                         // past the last pair
   const int r = p.row_begin + B->row;
   const int mp = B->pair;
   const int q0 = p.cu_seqlens_q[r];
@@ -329,7 +322,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
   const int L = p.seq_lens[r];
   if (!row_fits(p, q0, q_len, L)) {
     if (threadIdx.x == 0 && mp == 0 && g == 0 && split == 0) set_error(p.error_word, CB_DEVERR_SEQ_RANGE);
-    order_after_previous_grid();
     return;
   }
   const int tok0 = mp * tpp;                      // first token of the CTA
@@ -338,10 +330,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
   const int last_tok = min(tok0 + tpp - 1, q_len - 1);
   const int npages = (L + kPage - 1) / kPage;
   const Tiles tiles = tiles_of(p, start, q_len, tok0, tpp);
-  if (split >= tiles.splits) {
-    order_after_previous_grid();
-    return;
-  }
+  if (split >= tiles.splits) return;
   const int lo_pg = tiles.key_lo / kPage;
   const int j_lo = tiles.first + split * tiles.of_split;
   const int n_tiles = min(tiles.last, j_lo + tiles.of_split);
@@ -934,7 +923,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
   __syncthreads();
   tc::fence_after_sync();
   if (warp == kMmaWarp) tc::tmem_dealloc(tmem, kTmemCols);
-  order_after_previous_grid();
 }
 
 // Joins the splits' parts of the prefill rows' outputs: one warp for each
@@ -1001,27 +989,9 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ Param
 
 namespace {
 
-template <typename T, int D>
-cb_status launch_kernel(const cb_attention_args& a, const uint8_t* k_scales, const uint8_t* v_scales,
-                        int64_t scale_stride, const Parts& parts, uint32_t* error_word,
-                        cudaStream_t stream, bool overlap_previous) {
-  auto kern = prefill_kernel<T, D>;
-  static std::atomic<uint8_t> attr_set[kMaxDevices];
-  cb_status st = ensure_smem_attr(reinterpret_cast<const void*>(kern), Smem<D>::total, attr_set);
-  if (st != CB_OK) return st;
-  const int64_t n = ctas(a) * parts.splits;
-  if (n <= 0) return CB_OK;
-  if (n >= ((int64_t)1 << 31)) return CB_ERR_UNSUPPORTED;
-  const int64_t rows = (int64_t)a.num_blocks * a.num_kv_heads * kPage;
-  if (rows >= ((int64_t)1 << 31) - kPage) return CB_ERR_UNSUPPORTED;
-  Params p{};
-  st = cached_cache_map(&p.tmap_k, a.k_cache, rows, D, 1);
-  if (st != CB_OK) return st;
-  st = cached_cache_map(&p.tmap_v, a.v_cache, rows, D, 1);
-  if (st != CB_OK) return st;
-  p.k_scales = k_scales;
-  p.v_scales = v_scales;
-  p.scale_stride = scale_stride;
+// What the prefill kernel and the joining one both read.
+void set_call(const cb_attention_args& a, const Parts& parts, Params* out) {
+  Params& p = *out;
   p.q = a.q;
   p.out = a.out;
   p.cu_seqlens_q = a.cu_seqlens_q;
@@ -1042,26 +1012,35 @@ cb_status launch_kernel(const cb_attention_args& a, const uint8_t* k_scales, con
   p.splits = parts.splits;
   p.part_ml = parts.ml;
   p.part_acc = parts.acc;
+}
+
+template <typename T, int D>
+cb_status launch_kernel(const cb_attention_args& a, const uint8_t* k_scales, const uint8_t* v_scales,
+                        int64_t scale_stride, const Parts& parts, uint32_t* error_word,
+                        cudaStream_t stream) {
+  auto kern = prefill_kernel<T, D>;
+  static std::atomic<uint8_t> attr_set[kMaxDevices];
+  cb_status st = ensure_smem_attr(reinterpret_cast<const void*>(kern), Smem<D>::total, attr_set);
+  if (st != CB_OK) return st;
+  const int64_t n = ctas(a) * parts.splits;
+  if (n <= 0) return CB_OK;
+  if (n >= ((int64_t)1 << 31)) return CB_ERR_UNSUPPORTED;
+  const int64_t rows = (int64_t)a.num_blocks * a.num_kv_heads * kPage;
+  if (rows >= ((int64_t)1 << 31) - kPage) return CB_ERR_UNSUPPORTED;
+  Params p{};
+  st = cached_cache_map(&p.tmap_k, a.k_cache, rows, D, 1);
+  if (st != CB_OK) return st;
+  st = cached_cache_map(&p.tmap_v, a.v_cache, rows, D, 1);
+  if (st != CB_OK) return st;
+  p.k_scales = k_scales;
+  p.v_scales = v_scales;
+  p.scale_stride = scale_stride;
+  set_call(a, parts, &p);
   p.error_word = error_word;
   p.wait_ns = wait_limit_ns();
   p.withhold_tile = withheld_prefill_tile();
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)n, 1, 1);
-  cfg.blockDim = dim3(kThreads, 1, 1);
-  cfg.dynamicSmemBytes = Smem<D>::total;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = overlap_previous ? 1 : 0;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, kern, p);
-  if (e == cudaSuccess) e = cudaGetLastError();
-  if (e == cudaSuccess && parts.splits > 1) {
-    const int64_t warps = (int64_t)a.num_tokens * a.num_q_heads;
-    join_kernel<T, D><<<(unsigned)((warps + 7) / 8), 256, 0, stream>>>(p);
-    e = cudaGetLastError();
-  }
+  kern<<<(unsigned)n, kThreads, Smem<D>::total, stream>>>(p);
+  const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return fail(CB_ERR_CUDA, "prefill kernel launch: %s", cudaGetErrorString(e));
   return CB_OK;
 }
@@ -1092,11 +1071,10 @@ int splits(const cb_attention_args& a, int64_t slots) {
 }
 
 cb_status launch(const cb_attention_args& a, const uint8_t* k_scales, const uint8_t* v_scales,
-                 int64_t scale_stride, const Parts& parts, uint32_t* error_word, cudaStream_t stream,
-                 bool overlap_previous) {
+                 int64_t scale_stride, const Parts& parts, uint32_t* error_word, cudaStream_t stream) {
   if (a.num_q_heads / a.num_kv_heads > kBM) return CB_ERR_UNSUPPORTED;
 #define CB_PRE(T, DD) \
-  return launch_kernel<T, DD>(a, k_scales, v_scales, scale_stride, parts, error_word, stream, overlap_previous)
+  return launch_kernel<T, DD>(a, k_scales, v_scales, scale_stride, parts, error_word, stream)
   if (a.dtype == CB_DTYPE_F32) {
     if (a.head_dim == 64) CB_PRE(float, 64);
     CB_PRE(float, 128);
@@ -1104,6 +1082,22 @@ cb_status launch(const cb_attention_args& a, const uint8_t* k_scales, const uint
   if (a.head_dim == 64) CB_PRE(__nv_bfloat16, 64);
   CB_PRE(__nv_bfloat16, 128);
 #undef CB_PRE
+}
+
+cb_status join(const cb_attention_args& a, const Parts& parts, cudaStream_t stream) {
+  Params p{};
+  set_call(a, parts, &p);
+  const unsigned n = (unsigned)(((int64_t)a.num_tokens * a.num_q_heads + 7) / 8);
+  if (a.dtype == CB_DTYPE_F32) {
+    if (a.head_dim == 64) join_kernel<float, 64><<<n, 256, 0, stream>>>(p);
+    else join_kernel<float, 128><<<n, 256, 0, stream>>>(p);
+  } else {
+    if (a.head_dim == 64) join_kernel<__nv_bfloat16, 64><<<n, 256, 0, stream>>>(p);
+    else join_kernel<__nv_bfloat16, 128><<<n, 256, 0, stream>>>(p);
+  }
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return fail(CB_ERR_CUDA, "prefill join launch: %s", cudaGetErrorString(e));
+  return CB_OK;
 }
 
 }  // namespace prefill_q8

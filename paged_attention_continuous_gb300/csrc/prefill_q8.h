@@ -26,12 +26,14 @@ struct Parts {
 };
 
 // Rows [num_decodes, num_reqs) of `a`.  Returns CB_ERR_UNSUPPORTED (without a
-// message) for more than 128 query heads to a KV head.  overlap_previous: the
-// kernel queued just before on `stream` is the decode kernel of the same
-// call, which this grid may overlap (programmatic stream serialization).
+// message) for more than 128 query heads to a KV head.  The grid allows a
+// kernel launched behind it with programmatic stream serialization to start
+// when its last CTAs have started.
 cb_status launch(const cb_attention_args& a, const uint8_t* k_scales, const uint8_t* v_scales,
-                 int64_t scale_stride, const Parts& parts, uint32_t* error_word, cudaStream_t stream,
-                 bool overlap_previous);
+                 int64_t scale_stride, const Parts& parts, uint32_t* error_word, cudaStream_t stream);
+
+// Joins the parts of a launch with splits, once it has completed.
+cb_status join(const cb_attention_args& a, const Parts& parts, cudaStream_t stream);
 
 }  // namespace prefill_q8
 }  // namespace cb
