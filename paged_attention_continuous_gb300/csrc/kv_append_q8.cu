@@ -12,7 +12,7 @@
 // (a block's largest value is met early, so few appends do).  The runs of a
 // CTA's tokens are counted first and (run, head) dealt to the warps: dealt
 // by token instead, some warps wrote two runs one after the other while
-// others had none (8192 tokens below: 14.9 us).
+// others had none (the 6.9k tokens below took 14.9 us).
 //
 // With a rotary plan, k turns in registers before its magnitude is taken, a
 // lane holding both elements of its pairs, and k is neither written nor read
@@ -23,8 +23,8 @@
 // Every new element is read once and every code written once; HBM bounds
 // large calls and the launch with two dependent loads (slots, then the
 // block's scale) small ones.  Measured on the GPU alone, bf16, 8 heads of
-// 128: 8192 tokens 10.6 us (4.0 TB/s), 96 tokens with 32 heads of q turned
-// 4.5 us, 8192 tokens with 32 heads of q turned 33.5 us (4.6 TB/s).
+// 128: 6.9k tokens of 16 chunks 10.6 us (4.0 TB/s), 96 tokens with 32 heads
+// of q turned 4.5 us, the 6.9k with 32 heads of q turned 33.5 us (4.6 TB/s).
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -405,7 +405,12 @@ extern "C" cb_status cb_kv_append_q8(const cb_append_q8_args* args, cb_stream_t 
     p.q_rows.q_stride = p.q_rows.q_out_stride = (int64_t)a.num_q_heads * a.head_dim;
   }
   p.error_word = a.error_word;
-  p.tokens_per_cta = a.num_tokens <= 1024 ? 1 : kMaxTokens;
+  // Decode steps bring runs of one token and want a warp for each, chunks
+  // runs of 16 whose other tokens leave warps idle; the call cannot tell them
+  // apart.  96 decodes take 4.4 / 5.9 / 15.4 us with 1 / 4 / 16 tokens to a CTA,
+  // 1024 16.1 / 14.8 / 21.1, a chunk of 1000 tokens 5.8 / 5.0 / 3.8, 2048
+  // decodes 32.1 / 28.3 / 27.8, chunks of 2000 in all 8.2 / 6.1 / 4.4.
+  p.tokens_per_cta = a.num_tokens <= 256 ? 1 : a.num_tokens <= 1024 ? 4 : kMaxTokens;
   const bool f32 = a.dtype == CB_DTYPE_F32;
   const cudaStream_t s = (cudaStream_t)stream;
   if (a.head_dim == 64)

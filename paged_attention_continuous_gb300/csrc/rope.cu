@@ -8,6 +8,11 @@
 // vectors that hold the two halves of 8 (bf16) or 4 (f32) pairs; in the
 // interleaved one a vector holds whole pairs.  The first vectors are loaded
 // before the angles are computed, so their latencies overlap.
+// Measured on the GPU alone, bf16, 128 dims: 8192 tokens of 64 + 8 heads 50.8
+// us interleaved with half of the dims rotated (5.9 TB/s, 89% of the measured
+// copy rate; every element, rotated or not, is read and written), 48.0 in the
+// half layout and 50.4 interleaved with all rotated; 64 tokens of 32 + 8
+// heads 2.8 us.
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -67,7 +72,8 @@ cb_status launch(Params& p, cudaStream_t stream) {
   Rows& r = p.rows;
   cut_rows(&r, N, kHalf);
   // tokens per CTA: one while the tokens fit the SMs' resident CTAs once
-  // (latency), then four, so that a CTA's loads cover its set-up
+  // (latency: 64 tokens 2.5 us, 3.8 with four; 608 3.3 and 3.9), then four, so
+  // that a CTA's loads cover its set-up (2048 tokens 10.6 us with one, 9.5)
   p.tokens_per_cta = p.num_tokens <= 8 * sm_count_current_device() ? 1 : 4;
   const uint64_t items = (uint64_t)p.tokens_per_cta * r.heads * r.units;
   if (items * (uint64_t)(r.units > r.heads ? r.units : r.heads) >= 0x100000000ull)
