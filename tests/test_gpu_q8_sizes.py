@@ -1,12 +1,14 @@
 """cb_kv_append_q8 over token counts and head counts between the small and the
 large ones: runs that begin in one CTA's tokens and end in another's, heads
-that do not divide a CTA's warps, many heads."""
+that do not divide a CTA's warps, many heads; and cb_paged_attention_q8 with
+scales that are not ordinary, in place, and twice in a row."""
 import numpy as np
 import pytest
 
 torch = pytest.importorskip("torch")
 import paged_attention_continuous_gb300 as cb  # noqa: E402
 from tests import q8_reference as ref  # noqa: E402
+from tests.test_gpu_attention_q8_parts import Case  # noqa: E402
 from tests.test_gpu_append_q8 import DT, Pool, rows, slots_of  # noqa: E402
 from tests.test_gpu_rope import check as check_rope  # noqa: E402
 
@@ -84,3 +86,36 @@ def test_rotation_in_place_over_many_tokens(total, layout, dtype):
     b.append(kr.cpu(), v.float(), slots)
     assert torch.equal(a.cache[0].view(torch.uint8), b.cache[0].view(torch.uint8))
     assert torch.equal(a.wide[0], b.wide[0])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("scale", [0.0, -0.11, 2.0 ** -40])
+def test_attention_scales_that_are_not_ordinary(scale, dtype):
+    """Scale 0 and one far too small give the values' mean, a negative one
+    turns the order round."""
+    c = Case([(300, 1), (17, 1), (1200, 1), (400, 70), (2100, 9)], 3, 8, 2, 128, dtype, seed=41, spread=0.25)
+    c.scale = scale
+    c.check(c.run())
+    assert c.ws.read_errors() == 0
+
+
+def test_output_in_the_place_of_the_queries():
+    c = Case([(900, 1), (40, 1), (3000, 33), (200, 150)], 2, 16, 4, 64, "bf16", seed=42)
+    q = c.q.cuda()
+    assert c.run(q=q, out=q) is q
+    c.check(q)
+
+
+def test_two_calls_of_one_workspace_in_a_row():
+    """The second call may not start before the first is done with the
+    workspace, whatever each one's kernels are."""
+    a = Case([(5000, 1), (3000, 20)], 1, 8, 2, 128, "bf16", seed=43)
+    b = Case([(700, 1), (9000, 7)], 1, 8, 2, 128, "bf16", seed=44)
+    qa, qb = a.q.cuda(), b.q.cuda()
+    oa, ob = torch.zeros_like(qa), torch.zeros_like(qb)
+    for _ in range(20):
+        a.run(q=qa, out=oa)
+        b.run(q=qb, out=ob, workspace=a.ws)
+    a.check(oa)
+    b.check(ob)
+    assert a.ws.read_errors() == 0
