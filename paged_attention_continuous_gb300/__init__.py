@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional, Sequence
 
 import numpy as np
@@ -205,12 +206,13 @@ def _declare():
     L.cb_paged_attention.argtypes = [P(cb_attention_args), vp]
     L.cb_attention_read_errors.argtypes = [vp, sz, vp, P(ctypes.c_uint32)]
     L.cb_debug_inject_wait_timeout.argtypes = [ctypes.c_uint64, i32, i32]
-    L.cb_step_tables.argtypes = [P(cb_tables), vp, i32, vp, vp, vp, vp, vp]
-    L.cb_trim_tables.argtypes = [P(cb_tables), vp, vp]
+    # (the next ones are given packed structures, see _packer)
+    L.cb_step_tables.argtypes = [vp, vp, i32, vp, vp, vp, vp, vp]
+    L.cb_trim_tables.argtypes = [vp, vp, vp]
+    L.cb_rope.argtypes = [vp, vp]
+    L.cb_kv_append_q8.argtypes = [vp, vp]
+    L.cb_paged_attention_q8.argtypes = [vp, vp, vp, i64, vp]
     L.cb_rope_plan_init.argtypes = [P(cb_rope_config), P(cb_rope_plan)]
-    L.cb_rope.argtypes = [P(cb_rope_args), vp]
-    L.cb_kv_append_q8.argtypes = [P(cb_append_q8_args), vp]
-    L.cb_paged_attention_q8.argtypes = [P(cb_attention_args), vp, vp, i64, vp]
     PV = P(vp)
     L.cb_executor_create.argtypes = [P(cb_executor_config), P(vp)]
     L.cb_executor_destroy.argtypes = [vp]
@@ -571,7 +573,22 @@ def paged_attention(q, k_cache, v_cache, cu_seqlens_q, seq_lens, block_tables, *
 # ------------------------------------------- the 8-bit cache and its operators
 # A decode step makes these calls with a GPU that is done in a few
 # microseconds, so a call looks at each tensor once, by its cheapest
-# properties, and words an error only after one is found.
+# properties, words an error only after one is found, and packs its
+# arguments' structure in one step (0.3 us; 1.9 field by field).
+def _packer(structure):
+    """pack(field values, in order) -> the structure's bytes; pointers are
+    addresses (0: none)."""
+    code = {ctypes.c_int32: "i", ctypes.c_int64: "q", ctypes.c_float: "f", ctypes.c_double: "d",
+            ctypes.c_size_t: "N"}
+    s = struct.Struct("@" + "".join(code.get(t, "P") for _, t in structure._fields_))
+    assert s.size <= ctypes.sizeof(structure) < s.size + 8
+    return s.pack
+
+
+_pack_tables, _pack_rope = _packer(cb_tables), _packer(cb_rope_args)
+_pack_append, _pack_attention = _packer(cb_append_q8_args), _packer(cb_attention_args)
+
+
 def _launch_on(t, stream) -> int:
     """Device index of t, which has to be the current device (the launch goes
     to its stream), and the stream to launch on."""
@@ -579,7 +596,7 @@ def _launch_on(t, stream) -> int:
     dev = t.get_device()
     if dev < 0:
         raise ValueError("tensors must live on the GPU (no CPU path)")
-    if dev != torch.cuda.current_device():
+    if dev != torch._C._cuda_getDevice():
         raise ValueError("the tensors' device is not the current device")
     if stream is None:
         return dev, torch._C._cuda_getCurrentRawStream(dev)
@@ -613,7 +630,7 @@ def _i32(dev, named):
 
 def _error_ptr(error_word, dev):
     if error_word is None:
-        return None
+        return 0
     if error_word.get_device() != dev or error_word.element_size() != 4 or error_word.numel() < 1:
         raise ValueError("error_word must be a 4-byte word on the same device")
     return error_word.data_ptr()
@@ -624,7 +641,7 @@ def _tables(dev, cached_lens, block_tables, free_ring, free_state, block_size, e
     N = free_ring.numel()
     p = _i32(dev, (("cached_lens", cached_lens, R), ("block_tables", block_tables, R * W),
                    ("free_ring", free_ring, N), ("free_state", free_state, 2)))
-    return R, cb_tables(R, W, N, block_size, *p, _error_ptr(error_word, dev))
+    return R, _pack_tables(R, W, N, block_size, *p, _error_ptr(error_word, dev))
 
 
 def step_tables(q_lens, cached_lens, block_tables, free_ring, free_state, *, cu_seqlens_q,
@@ -641,7 +658,7 @@ def step_tables(q_lens, cached_lens, block_tables, free_ring, free_state, *, cu_
     q, cu, seq, slots, pos = _i32(dev, (("q_lens", q_lens, R), ("cu_seqlens_q", cu_seqlens_q, R + 1),
                                         ("seq_lens", seq_lens, R), ("slot_mapping", slot_mapping, T),
                                         ("positions", positions, T)))
-    _check(_lib.cb_step_tables(ctypes.byref(t), q, T, cu, seq, slots, pos, st))
+    _check(_lib.cb_step_tables(t, q, T, cu, seq, slots, pos, st))
 
 
 def trim_tables(keep_lens, cached_lens, block_tables, free_ring, free_state, *,
@@ -652,7 +669,7 @@ def trim_tables(keep_lens, cached_lens, block_tables, free_ring, free_state, *,
     dev, st = _launch_on(cached_lens, stream)
     R, t = _tables(dev, cached_lens, block_tables, free_ring, free_state, block_size, error_word)
     keep, = _i32(dev, (("keep_lens", keep_lens, R),))
-    _check(_lib.cb_trim_tables(ctypes.byref(t), keep, st))
+    _check(_lib.cb_trim_tables(t, keep, st))
 
 
 ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
@@ -679,6 +696,7 @@ class RopePlan:
         self.c = cb_rope_plan()
         _check(_lib.cb_rope_plan_init(ctypes.byref(c), ctypes.byref(self.c)))
         self._p = ctypes.pointer(self.c)
+        self._at = ctypes.addressof(self.c)
 
     @property
     def head_dim(self) -> int:
@@ -721,7 +739,7 @@ def rope(q, k, positions, plan: RopePlan, *, q_out=None, k_out=None, inverse: bo
         raise ValueError("neither q nor k is given")
     dev, st = _launch_on(first, stream)
     T, d, dtype = first.shape[0], plan.c.head_dim, first.dtype
-    qa = ka = (None, None, 0, 0, 0)
+    qa = ka = (0, 0, 0, 0, 0)
     if q is not None:
         if q_out is None:
             q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
@@ -731,8 +749,8 @@ def rope(q, k, positions, plan: RopePlan, *, q_out=None, k_out=None, inverse: bo
             k_out = torch.empty_like(k, memory_format=torch.contiguous_format)
         ka = _rope_rows("k", k, k_out, dev, T, d, dtype)
     pos, = _i32(dev, (("positions", positions, T),))
-    a = cb_rope_args(plan._p, pos, T, qa[4], ka[4], _dtype_code(first), 1 if inverse else 0, *qa[:4], *ka[:4])
-    _check(_lib.cb_rope(ctypes.byref(a), st))
+    a = _pack_rope(plan._at, pos, T, qa[4], ka[4], _dtype_code(first), 1 if inverse else 0, *qa[:4], *ka[:4])
+    _check(_lib.cb_rope(a, st))
     return q_out, k_out
 
 
@@ -789,12 +807,11 @@ def kv_append_q8(k_new, v_new, slot_mapping, k_cache, v_cache, k_scales, v_scale
     slots, = _i32(dev, (("slot_mapping", slot_mapping, T),))
     kp = _rows3("k_new", k_new, dev, dtype, T, hkv, d)
     vp = _rows3("v_new", v_new, dev, dtype, T, hkv, d)
-    plan = pos = qp = op = None
-    hq = 0
+    plan = pos = qp = op = hq = 0
     if rope is not None:
         if positions is None:
             raise ValueError("rope needs positions")
-        plan = rope._p
+        plan = rope._at
         pos, = _i32(dev, (("positions", positions, T),))
         if q is not None:
             if q_out is None:
@@ -804,9 +821,9 @@ def kv_append_q8(k_new, v_new, slot_mapping, k_cache, v_cache, k_scales, v_scale
             op = _rows3("q_out", q_out, dev, dtype, T, hq, d)
     elif q is not None or positions is not None:
         raise ValueError("q and positions go with rope")
-    a = cb_append_q8_args(kp, vp, slots, T, _dtype_code(k_new), kc, vc, ks, vs, ss, nb, hkv, d, bs,
-                          plan, pos, qp, op, hq, _error_ptr(error_word, dev))
-    _check(_lib.cb_kv_append_q8(ctypes.byref(a), st))
+    a = _pack_append(kp, vp, slots, T, _dtype_code(k_new), kc, vc, ks, vs, ss, nb, hkv, d, bs,
+                     plan, pos, qp, op, hq, _error_ptr(error_word, dev))
+    _check(_lib.cb_kv_append_q8(a, st))
     return q_out if q is not None else None
 
 
@@ -830,10 +847,10 @@ def paged_attention_q8(q, k_cache, v_cache, k_scales, v_scales, cu_seqlens_q, se
         raise ValueError("workspace sized for fewer requests")
     if workspace.buf.get_device() != dev:
         raise ValueError("tensors live on different devices")
-    a = cb_attention_args(qp, op, kc, vc, cu, seq, bt, R, num_decodes, T, max_q_len, max_seq_len,
+    a = _pack_attention(qp, op, kc, vc, cu, seq, bt, R, num_decodes, T, max_q_len, max_seq_len,
                           nb, W, bs, hq, hkv, d, scale, _dtype_code(q), workspace.ptr,
                           workspace.nbytes, sliding_window, 1 if after_append else 0)
-    _check(_lib.cb_paged_attention_q8(ctypes.byref(a), ks, vs, ss, st))
+    _check(_lib.cb_paged_attention_q8(a, ks, vs, ss, st))
     return out
 
 
