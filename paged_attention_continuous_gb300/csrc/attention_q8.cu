@@ -146,8 +146,8 @@ extern "C" cb_status cb_paged_attention_q8(const cb_attention_args* args, const 
     if (st != CB_OK) return st;
   }
   // Decode rows run the split-KV kernel, the others the prefill kernel; what
-  // those two do not take (KV heads shared by very many query heads) runs
-  // the row kernel.  The prefill rows come first: the decode kernel then takes
+  // those two do not take (KV heads shared by very many query heads; for
+  // decodes more than 64 items to a split) runs the row kernel.  The prefill rows come first: the decode kernel then takes
   // the SMs that they leave, item by item, from the last wave's start on (96
   // decodes and 2.9k prompt tokens 218 us, 232 in the other order; with 512
   // tokens behind 4k 179 and 212, behind 15k 257 and 385; 64 decodes and 600

@@ -99,6 +99,22 @@ def test_attention_scales_that_are_not_ordinary(scale, dtype):
     assert c.ws.read_errors() == 0
 
 
+@pytest.mark.parametrize("hq,hkv", [(64, 64), (160, 1), (272, 17), (561, 33)])
+def test_many_heads_of_attention(hq, hkv):
+    """As many KV heads as a call may have; groups that the decode kernel
+    serves in parts, and (160, 561) that it or the prefill kernel does not."""
+    c = Case([(90, 1), (700, 1), (120, 40), (2100, 3)], 2, hq, hkv, 64, "bf16", seed=45)
+    c.check(c.run())
+    assert c.ws.read_errors() == 0
+
+
+@pytest.mark.parametrize("hq,hkv", [(72, 72), (130, 65)])
+def test_too_many_kv_heads_are_refused(hq, hkv):
+    c = Case([(90, 1), (120, 40)], 1, hq, hkv, 64, "bf16", seed=46)
+    with pytest.raises(cb.CBError, match="num_kv_heads > 64"):
+        c.run()
+
+
 def test_output_in_the_place_of_the_queries():
     c = Case([(900, 1), (40, 1), (3000, 33), (200, 150)], 2, 16, 4, 64, "bf16", seed=42)
     q = c.q.cuda()
