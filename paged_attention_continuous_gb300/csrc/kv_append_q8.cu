@@ -72,7 +72,7 @@ struct Params {
 template <typename T, int kRope>
 __device__ __forceinline__ void rotate_q(const Params& p, int t0, int tokens, float2* cs) {
   constexpr int N = Vec<T>::kN;
-  constexpr int kAhead = kRope == kHalf ? 2 : 4;  // 64 bytes of loads in flight per thread
+  constexpr int kAhead = 2;  // 64 bytes of loads in flight per thread
   const uint32_t items = (uint32_t)tokens * p.q_rows.heads * p.q_rows.units;
   rope::Unit<T, N> w[kAhead];
   uint32_t n = threadIdx.x;

@@ -6,12 +6,14 @@
 // -- the only work per (token, pair), shared by every head of q and k -- and
 // then move vectors of 16 bytes.  In the half layout a thread owns the two
 // vectors that hold the two halves of 8 (bf16) or 4 (f32) pairs; in the
-// interleaved one a vector holds whole pairs.  The first vectors are loaded
-// before the angles are computed, so their latencies overlap.
-// Measured on the GPU alone, bf16, 128 dims: 8192 tokens of 64 + 8 heads 50.8
-// us interleaved with half of the dims rotated (5.9 TB/s, 89% of the measured
-// copy rate; every element, rotated or not, is read and written), 48.0 in the
-// half layout and 50.4 interleaved with all rotated; 64 tokens of 32 + 8
+// interleaved one a vector holds whole pairs, and a thread owns two that lie
+// half a row apart (one vector to a thread: 51.2 us where it takes 47.2
+// below).  The first vectors are loaded before the angles are computed, so
+// their latencies overlap.
+// Measured on the GPU alone, bf16, 128 dims: 8192 tokens of 64 + 8 heads 47.2
+// us interleaved with half of the dims rotated (6.4 TB/s, 96% of the measured
+// copy rate; every element, rotated or not, is read and written), 47.8 in the
+// half layout and 48.8 interleaved with all rotated; 64 tokens of 32 + 8
 // heads 2.8 us.
 #include <cuda_runtime.h>
 
@@ -41,7 +43,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
   const int t0 = (int)blockIdx.x * p.tokens_per_cta;
   const int tokens = min(p.tokens_per_cta, p.num_tokens - t0);
   const uint32_t items = (uint32_t)tokens * p.rows.heads * p.rows.units;
-  constexpr int kAhead = N == 1 ? 1 : kHalf ? 2 : 4;  // 64 bytes of loads in flight per thread
+  constexpr int kAhead = N == 1 ? 1 : 2;  // 64 bytes of loads in flight per thread
   Unit<T, N> w[kAhead];
   uint32_t n = threadIdx.x;
 #pragma unroll

@@ -71,8 +71,10 @@ __device__ __forceinline__ void from_float(float* p, float x) { *p = x; }
 __device__ __forceinline__ void from_float(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
 
 // ---- rows of q (and k) as units of work ------------------------------------
-// The rows of a few tokens, cut into units that one thread moves: rot_units
-// per head row that rotate, then units that are only copied.
+// The rows of a few tokens, cut into units that one thread moves.  In the
+// half layout (and for single elements): rot_units per head row that rotate,
+// then units that are only copied.  Interleaved vectors: vector u of a row and
+// the one half a row further on, of which the first rot_units rotate.
 struct Rows {
   int32_t head_dim, rot_dim;
   int32_t hq, heads;                  // heads of q (0 without q), of q and k together
@@ -88,7 +90,7 @@ struct Rows {
 // Fills units, rot_units and the magics for units of N elements.
 inline void cut_rows(Rows* r, int n, bool half) {
   r->rot_units = half ? r->rot_dim / 2 / n : n > 1 ? r->rot_dim / n : r->rot_dim / 2;
-  r->units = r->rot_units + (r->head_dim - r->rot_dim) / n;
+  r->units = !half && n > 1 ? (r->head_dim / n + 1) / 2 : r->rot_units + (r->head_dim - r->rot_dim) / n;
   auto magic = [](int d) { return d == 1 ? 0u : (uint32_t)((0x100000000ull + d - 1) / d); };
   r->units_magic = magic(r->units);
   r->heads_magic = magic(r->heads);
@@ -110,13 +112,14 @@ __device__ __forceinline__ uint32_t div_by(uint32_t n, uint32_t magic) {
   return magic ? __umulhi(n, magic) : n;
 }
 
-// A unit of work: N elements at `a`, and their partners at `b` when it
-// rotates in the half layout (or N = 1, for rows that vectors do not fit: one
-// pair, or one element to copy).  pair < 0: a unit that is only copied.
+// A unit of work: N elements at `a`, and at `b` (unless negative) their
+// partners in the half layout, other N elements in the interleaved one, or (N
+// = 1, for rows that vectors do not fit) the other of a pair.  pair < 0: what
+// is only copied.
 template <typename T, int N>
 struct Unit {
   T* out;
-  int a, b, pair;
+  int a, b, pair, pair_b;
   bool same;        // in place
   uint4 x, y;       // N elements each, as they lie in memory (N = 1: one float)
 };
@@ -139,16 +142,21 @@ __device__ __forceinline__ void load_unit(const Rows& p, int t0, uint32_t n, Uni
   }
   w.same = in == w.out;
   w.b = -1;
-  if (u >= p.rot_units) {
+  const int angles = (int)tl * (rot / 2);  // this token's in shared memory
+  if constexpr (!kHalf && N > 1) {
+    const int v = u + p.units;
+    w.a = u * N;
+    w.b = v * N < D ? v * N : -1;
+    w.pair = u < p.rot_units ? angles + u : -1;
+    w.pair_b = v < p.rot_units ? angles + v : -1;
+  } else if (u >= p.rot_units) {
     w.a = rot + (u - p.rot_units) * N;
     w.pair = -1;
   } else {
-    w.pair = (int)tl * (rot / 2) + u;  // the unit's first angle in shared memory
+    w.pair = angles + u;  // the unit's first angle
     if (kHalf) {
       w.a = u * N;
       w.b = w.a + rot / 2;
-    } else if (N > 1) {
-      w.a = u * N;
     } else {
       w.a = 2 * u;
       w.b = w.a + 1;
@@ -156,7 +164,7 @@ __device__ __forceinline__ void load_unit(const Rows& p, int t0, uint32_t n, Uni
   }
   if constexpr (N > 1) {
     w.x = *reinterpret_cast<const uint4*>(in + w.a);
-    if (kHalf && w.b >= 0) w.y = *reinterpret_cast<const uint4*>(in + w.b);
+    if (w.b >= 0) w.y = *reinterpret_cast<const uint4*>(in + w.b);
   } else {
     w.x.x = __float_as_uint(to_float(in[w.a]));
     if (w.b >= 0) w.y.x = __float_as_uint(to_float(in[w.b]));
@@ -171,21 +179,31 @@ __device__ __forceinline__ void store_unit(const float2* cs, int stride, const U
     if (w.pair >= 0) rotate(x, y, cs[w.pair]);
     from_float(w.out + w.a, x);
     if (w.b >= 0) from_float(w.out + w.b, y);
-  } else if (w.pair < 0) {
-    *reinterpret_cast<uint4*>(w.out + w.a) = w.x;
-  } else {
+  } else if constexpr (kHalf) {
+    if (w.pair < 0) {
+      *reinterpret_cast<uint4*>(w.out + w.a) = w.x;
+      return;
+    }
     float x[N], y[N];
     Vec<T>::load(w.x, x);
-    if constexpr (kHalf) {
-      Vec<T>::load(w.y, y);
+    Vec<T>::load(w.y, y);
 #pragma unroll
-      for (int i = 0; i < N; ++i) rotate(x[i], y[i], cs[w.pair + i * stride]);
-      *reinterpret_cast<uint4*>(w.out + w.b) = Vec<T>::store(y);
-    } else {
-#pragma unroll
-      for (int i = 0; i < N; i += 2) rotate(x[i], x[i + 1], cs[w.pair + i / 2 * stride]);
-    }
+    for (int i = 0; i < N; ++i) rotate(x[i], y[i], cs[w.pair + i * stride]);
+    *reinterpret_cast<uint4*>(w.out + w.b) = Vec<T>::store(y);
     *reinterpret_cast<uint4*>(w.out + w.a) = Vec<T>::store(x);
+  } else {
+    auto vector = [&](uint4 raw, int at, int pair) {
+      if (pair >= 0) {
+        float x[N];
+        Vec<T>::load(raw, x);
+#pragma unroll
+        for (int i = 0; i < N; i += 2) rotate(x[i], x[i + 1], cs[pair + i / 2 * stride]);
+        raw = Vec<T>::store(x);
+      }
+      if (pair >= 0 || !w.same) *reinterpret_cast<uint4*>(w.out + at) = raw;
+    };
+    vector(w.x, w.a, w.pair);
+    if (w.b >= 0) vector(w.y, w.b, w.pair_b);
   }
 }
 
