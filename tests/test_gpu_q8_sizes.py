@@ -1,7 +1,8 @@
 """cb_kv_append_q8 over token counts and head counts between the small and the
 large ones: runs that begin in one CTA's tokens and end in another's, heads
 that do not divide a CTA's warps, many heads; and cb_paged_attention_q8 with
-scales that are not ordinary, in place, and twice in a row."""
+scales that are not ordinary, in place, and twice in a row; and cb_rope over
+rows of an odd number of vectors."""
 import numpy as np
 import pytest
 
@@ -135,3 +136,23 @@ def test_two_calls_of_one_workspace_in_a_row():
     a.check(oa)
     b.check(ob)
     assert a.ws.read_errors() == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("D,rot", [(8, 8), (24, 8), (24, 16), (24, 24), (40, 32), (72, 64), (72, 16), (200, 112)])
+def test_rope_of_an_odd_number_of_vectors(D, rot, layout, dtype):
+    plan = cb.RopePlan(D, rot, layout=layout)
+    g = torch.Generator().manual_seed(47)
+    T, hq, hkv = 37, 3, 2
+    both = torch.randn(T, hq + hkv, D, generator=g).to(DT[dtype]).cuda()      # q and k in one array
+    q, k = both[:, :hq], both[:, hq:]
+    pos = np.random.default_rng(48).integers(-50, 1 << 20, T).astype(np.int32)
+    was = both.cpu()
+    for inverse in (False, True):
+        qo, ko = cb.rope(q, k, torch.tensor(pos).cuda(), plan, inverse=inverse)
+        check_rope(qo.double().cpu().numpy(), was[:, :hq].double().numpy(), pos, plan, layout, dtype, inverse)
+        check_rope(ko.double().cpu().numpy(), was[:, hq:].double().numpy(), pos, plan, layout, dtype, inverse)
+        assert torch.equal(ko[..., rot:].cpu(), was[:, hq:, rot:])
+    cb.rope(q, k, torch.tensor(pos).cuda(), plan, q_out=q, k_out=k, inverse=True)   # in place
+    assert torch.equal(both, torch.cat([qo, ko], 1))
