@@ -44,7 +44,9 @@
 //   * A value code that is NaN must not reach rows that do not see its key
 //     (weight 0 times NaN is NaN): in tiles that some row of the CTA sees only
 //     in part, converters store such codes as 0 and note the first and last
-//     key for each dim; the epilogue writes NaN where a row sees one.
+//     key for each dim; the epilogue writes NaN where a row sees one.  Between
+//     those two (with a window a row may see neither) it looks at the codes
+//     again, which only calls with several such codes in one dim pay for.
 //
 //   * Few rows with many keys would leave most SMs idle: when the CTAs fill
 //     less than half of them, each one's KV tiles are split over as many CTAs
@@ -157,6 +159,7 @@ static_assert(Smem<128>::total <= 227 * 1024, "shared memory");
 struct Params {
   CUtensorMap tmap_k;  // [num_blocks * Hkv * 16 rows][D] bytes, box 16 rows x D
   CUtensorMap tmap_v;
+  const uint8_t* v_cache;     // (the epilogue's second look at NaN codes)
   const uint8_t* k_scales;
   const uint8_t* v_scales;
   int64_t scale_stride;
@@ -248,6 +251,39 @@ __device__ __forceinline__ Tiles tiles_of(const Params& p, int start, int q_len,
   t.of_split = p.splits > 1 ? max((n + p.splits - 1) / p.splits, kLeastTiles) : n;
   t.splits = p.splits > 1 ? (n + t.of_split - 1) / t.of_split : 1;
   return t;
+}
+
+// Some row of the CTA does not see all keys of the tile that starts at kbase.
+__device__ __forceinline__ bool seen_in_part(const Params& p, const volatile Bars* B, int kbase) {
+  return kbase + kBN - 1 > B->first_pos || (p.window > 0 && kbase < B->last_pos - p.window + 1);
+}
+
+// Bit e: a value of dim d0 + e that the row at position pos sees in a tile
+// that is seen in part is NaN.  key_row: the first key of the row's window.
+template <int D>
+__device__ __forceinline__ uint32_t nan_dims(const Params& p, const volatile Bars* B, int g, int d0, int pos,
+                                             int key_row) {
+  uint32_t mask = 0;
+#pragma unroll 1
+  for (int e = 0; e < 32; ++e) {
+    const int first = B->nan_first[d0 + e], last = B->nan_last[d0 + e];
+    bool sees = (first <= pos && first >= key_row) || (last <= pos && last >= key_row && last >= 0);
+    if (!sees && first < key_row && last > pos) {
+      // neither end of the NaN keys is seen: one between them may be
+#pragma unroll 1
+      for (int key = key_row; key <= pos && !sees; ++key) {
+        if (!seen_in_part(p, B, key / kBN * kBN)) {
+          key |= kBN - 1;                         // such a tile's NaN codes were multiplied
+          continue;
+        }
+        const int b = p.block_tables[(int64_t)B->table_row * p.max_blocks_per_seq + key / kPage];
+        if (b >= 0 && b < p.num_blocks)
+          sees = (p.v_cache[(((int64_t)b * p.num_kv_heads + g) * kPage + key % kPage) * D + d0 + e] & 0x7f) == 0x7f;
+      }
+    }
+    mask |= (uint32_t)sees << e;
+  }
+  return mask;
 }
 
 template <typename T, int D>
@@ -484,8 +520,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       const uint32_t vt = Smem<D>::v + st * kTile;
       const int kbase = j * kBN;
       const int end = VB->seq_len - kbase;         // rows past the sequence become zeros
-      // some row of the CTA does not see all keys of this tile
-      const bool part = kbase + kBN - 1 > VB->first_pos || (p.window > 0 && kbase < VB->last_pos - p.window + 1);
+      const bool part = seen_in_part(p, VB, kbase);
       if (!part) {
 #pragma unroll
         for (int i = 0; i < kRounds; ++i) store(vt, i, w[i]);
@@ -876,6 +911,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         const bool any_nan = *reinterpret_cast<volatile int32_t*>(&B->nan_any) != 0;
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
+          const uint32_t nan = any_nan ? nan_dims<D>(p, VB, g, 32 * c, pos, key_row) : 0u;
+          __syncwarp();                           // (rows look at numbers of keys of their own)
           float o[32];
           tc::tmem_ld32_sync(trow + colO + 32 * c, o);
           if (kF32 && nt > 1) {
@@ -888,10 +925,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
           for (int e = 0; e < 32; ++e) o[e] *= inv;
           if (any_nan) {
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              const int a = B->nan_first[32 * c + e], b = B->nan_last[32 * c + e];
-              if ((a <= pos && a >= key_row) || (b >= 0 && b <= pos && b >= key_row)) o[e] = __int_as_float(0x7fffffff);
-            }
+            for (int e = 0; e < 32; ++e)
+              if (nan >> e & 1) o[e] = __int_as_float(0x7fffffff);
           }
           if (parted) {
             // 32 dims of this split's part, in float32, row by row
@@ -1032,6 +1067,7 @@ cb_status launch_kernel(const cb_attention_args& a, const uint8_t* k_scales, con
   if (st != CB_OK) return st;
   st = cached_cache_map(&p.tmap_v, a.v_cache, rows, D, 1);
   if (st != CB_OK) return st;
+  p.v_cache = static_cast<const uint8_t*>(a.v_cache);
   p.k_scales = k_scales;
   p.v_scales = v_scales;
   p.scale_stride = scale_stride;
