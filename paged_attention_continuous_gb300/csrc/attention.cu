@@ -12,6 +12,7 @@
 #include "device_utils.cuh"
 #include "launch_common.h"
 #include "prefill_dispatch.h"
+#include "row_checks.h"
 #include "simt_attention.cuh"
 #include "validate.h"
 
@@ -79,7 +80,7 @@ cb_status check_attention(const cb_attention_args& a) {
   if (a.num_blocks <= 0 || a.max_blocks_per_seq <= 0) return fail(CB_ERR_INVALID_ARG, "bad pool sizes");
   if (a.sliding_window < 0) return fail(CB_ERR_INVALID_ARG, "sliding_window must be >= 0");
   if (a.max_q_len < 1 || a.max_seq_len < a.max_q_len ||
-      (a.max_seq_len + a.block_size - 1) / a.block_size > a.max_blocks_per_seq)
+      blocks_of(a.max_seq_len, a.block_size) > a.max_blocks_per_seq)
     return fail(CB_ERR_INVALID_ARG, "max_q_len / max_seq_len inconsistent with the block table");
   const uintptr_t al = (uintptr_t)a.q | (uintptr_t)a.out | (uintptr_t)a.k_cache | (uintptr_t)a.v_cache;
   if (al & 15u) return fail(CB_ERR_INVALID_ARG, "q/out/cache pointers must be 16-byte aligned");

@@ -13,6 +13,7 @@
 #include "prefill_q8.h"
 #include "q8.cuh"
 #include "rope.cuh"
+#include "row_checks.h"
 #include "validate.h"
 
 namespace cb {
@@ -57,7 +58,7 @@ __global__ void __launch_bounds__(256) rows_kernel(const RowsParams p) {
   const int r = lo, q0 = p.cu_seqlens_q[r], q1 = p.cu_seqlens_q[r + 1];
   if (t < q0 || t >= q1 || r < p.row_begin || r >= p.row_end) return;
   const int L = p.seq_lens[r], q_len = q1 - q0;
-  if (L < q_len || (L + kPage - 1) / kPage > p.max_blocks_per_seq) {
+  if (L < q_len || !row_length_fits(L, kPage, p.max_blocks_per_seq)) {
     if (lane == 0) set_error(p.error_word, CB_DEVERR_SEQ_RANGE);
     return;
   }

@@ -418,7 +418,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_kernel(const __grid_con
     const int split = phase_a ? (int)u - a0 : (int)u - num_a - b0;
     const int r = p.row_begin + i;
     const int L = row_len[i];
-    const int pages = (L + kPageTokens - 1) / kPageTokens;
+    const int pages = blocks_of(L, kPageTokens);
     const int fp = first_page(L, win);
     const int na = a1 - a0;
     const int bp = fp + na * spa0;

@@ -387,7 +387,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_kernel(const __grid_con
     const int a0 = plan_a[i], na = plan_a[i + 1] - a0, b0 = plan_b[i], nb = plan_b[i + 1] - b0;
     const int split = phase_a ? (int)x - a0 : (int)x - num_a - b0;
     const int L = row_len[i];
-    const int fp = first_page(L, win), end = (L + kPageTokens - 1) / kPageTokens;
+    const int fp = first_page(L, win), end = blocks_of(L, kPageTokens);
     const RowSplit rs = row_split(end - fp, spa0, spb0, kPair);
     nx_ok = true;
     const int u = (int)(idx - x * (uint32_t)units);
@@ -562,7 +562,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_kernel(const __grid_con
       const ItemDesc& d = ws.items[cons_items % kRing];
       c_page = d.page0;
       c_end = d.page1;
-      c_lo = (first_key(d.seq_len, win) + kPageTokens - 1) / kPageTokens;
+      c_lo = blocks_of(first_key(d.seq_len, win), kPageTokens);
       c_hi = min(c_end, d.seq_len / kPageTokens);
       const T* q0 = static_cast<const T*>(p.q) + ((int64_t)d.token * Hq + d.h0) * D + 16 * qd;
 #pragma unroll

@@ -67,6 +67,7 @@
 #include "device_utils.cuh"
 #include "launch_common.h"
 #include "prefill_dispatch.h"
+#include "row_checks.h"
 #include "tcgen05.cuh"
 #include "tensor_map.h"
 
@@ -251,7 +252,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int q_len = p.cu_seqlens_q[r + 1] - q0;
   const int L = p.seq_lens[r];
   const int W = p.max_blocks_per_seq;
-  if (q0 < 0 || q0 + q_len > p.num_tokens || L < q_len || (L + kPage - 1) / kPage > W) {
+  if (!row_tokens_fit(q0, q_len, p.num_tokens) || L < q_len || !row_length_fits(L, kPage, W)) {
     if (threadIdx.x == 0 && mp == 0 && g == 0) set_error(p.error_word, CB_DEVERR_SEQ_RANGE);
     order_after_previous_grid();
     return;
@@ -265,7 +266,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int start = L - q_len;
   const int last_tok = min(tok0 + 2 * tpt - 1, q_len - 1);
   const int n_tiles = (start + last_tok) / kBN + 1;
-  const int npages = (L + kPage - 1) / kPage;
+  const int npages = blocks_of(L, kPage);
   // with a window, the pair's first query reads keys from key_lo on: KV
   // tiles j_lo .. n_tiles - 1 (nt of them; ring positions count from j_lo)
   const int key_lo = p.window > 0 ? max(0, start + tok0 - p.window + 1) : 0;
@@ -413,7 +414,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // sequence: zero them (both 64-dim halves) before P.V reads them
             // (both issuers write the same zeros)
             uint8_t* vt = smem + SmemLayout::v + sp * kTileBytes;
-            const int r0 = L - jp * kBN, r1 = ((L + kPage - 1) / kPage) * kPage - jp * kBN;
+            const int r0 = L - jp * kBN, r1 = (npages - jp * (kBN / kPage)) * kPage;
             for (int rw = r0; rw < r1; ++rw)
               for (int c = 0; c < 8; ++c) {
                 *reinterpret_cast<uint4*>(vt + rw * 128 + c * 16) = make_uint4(0, 0, 0, 0);

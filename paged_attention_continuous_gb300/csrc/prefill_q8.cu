@@ -88,6 +88,7 @@
 #include "prefill_q8.h"
 #include "q8.cuh"
 #include "rope.cuh"
+#include "row_checks.h"
 #include "tcgen05.cuh"
 #include "tensor_map.h"
 
@@ -230,8 +231,8 @@ __device__ __forceinline__ uint32_t nan_codes(uint32_t w) {
 // A row's tokens and length lie within the call's (and its parts' places).
 __device__ __forceinline__ bool row_fits(const Params& p, int q0, int q_len, int L) {
   const int first = p.splits > 1 ? p.cu_seqlens_q[p.row_begin] : 0;
-  return first >= 0 && q0 >= first && q_len <= p.num_tokens - q0 && L >= q_len &&
-         (L - 1) / kPage < p.max_blocks_per_seq;
+  return first >= 0 && q0 >= first && row_tokens_fit(q0, q_len, p.num_tokens) && L >= q_len &&
+         row_length_fits(L, kPage, p.max_blocks_per_seq);
 }
 
 // The KV tiles of a (row, pair of query tiles) and of each of its splits.
@@ -364,7 +365,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
   const bool has_t1 = kTiles == 2 && tok0 + tpt < q_len;
   const int start = L - q_len;
   const int last_tok = min(tok0 + tpp - 1, q_len - 1);
-  const int npages = (L + kPage - 1) / kPage;
+  const int npages = blocks_of(L, kPage);
   const Tiles tiles = tiles_of(p, start, q_len, tok0, tpp);
   if (split >= tiles.splits) return;
   const int lo_pg = tiles.key_lo / kPage;

@@ -15,6 +15,7 @@
 #include <cuda_bf16.h>
 
 #include "device_utils.cuh"
+#include "row_checks.h"
 
 namespace cb {
 namespace simt {
@@ -76,7 +77,7 @@ __global__ void __launch_bounds__(256) rows_kernel(const Params p) {
   const int L = p.seq_lens[r];
   const int bs = p.block_size;
   T* orow = static_cast<T*>(p.out) + ((int64_t)t * Hq + h) * D;
-  if (q_len < 1 || L < q_len || (L + bs - 1) / bs > p.max_blocks_per_seq) {
+  if (q_len < 1 || L < q_len || !row_length_fits(L, bs, p.max_blocks_per_seq)) {
     if (lane == 0) set_error(p.error_word, CB_DEVERR_SEQ_RANGE);
     for (int e = lane; e < D; e += 32) store_elem<T>(orow + e, 0.f);
     return;

@@ -7,6 +7,7 @@
 
 #include "decode_launch.h"
 #include "device_utils.cuh"
+#include "row_checks.h"
 
 namespace cb {
 namespace decode {
@@ -102,11 +103,10 @@ __device__ __forceinline__ SplitPlan plan_splits(const PlanRows& in, int nwarps,
     int L = in.seq_lens[r];
     const int q0 = in.cu_seqlens_q[r];
     const int q1 = in.cu_seqlens_q[r + 1];
-    int pages = (L + kPageTokens - 1) / kPageTokens;
     if (L == 0 && q1 == q0) {
       // a padding row (no query, no context): nothing to do
     } else {
-      if (L < 1 || pages > in.max_blocks) {
+      if (!row_length_fits(L, kPageTokens, in.max_blocks)) {
         L = 0;
         if (blockIdx.x == 0) set_error(in.error_word, CB_DEVERR_SEQ_RANGE);
       }
@@ -115,7 +115,7 @@ __device__ __forceinline__ SplitPlan plan_splits(const PlanRows& in, int nwarps,
         if (blockIdx.x == 0) set_error(in.error_word, CB_DEVERR_DECODE_QLEN);
       }
     }
-    pages = (L + kPageTokens - 1) / kPageTokens - first_page(L, in.window);
+    const int pages = blocks_of(L, kPageTokens) - first_page(L, in.window);
     row_len[i] = L;
     row_tok[i] = q0;
     my_pages += pages;
@@ -174,7 +174,7 @@ __device__ __forceinline__ SplitPlan plan_splits(const PlanRows& in, int nwarps,
     for (int i = b; i < e; ++i) {
       const int Li = row_len[i];
       const RowSplit rs =
-          row_split((Li + kPageTokens - 1) / kPageTokens - first_page(Li, in.window), spa0, spb0, in.even);
+          row_split(blocks_of(Li, kPageTokens) - first_page(Li, in.window), spa0, spb0, in.even);
       const int na = rs.na, nb = rs.nb;
       plan_a[i + 1] = na;
       plan_b[i + 1] = nb;
