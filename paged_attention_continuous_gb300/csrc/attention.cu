@@ -22,8 +22,8 @@ namespace {
 
 template <typename T, int D>
 cb_status launch_simt_rows(const cb_attention_args& a, const WsLayout& L, int row_begin,
-                           int row_end, int tok_begin, int tok_end, cudaStream_t stream) {
-  if (row_end <= row_begin || tok_end <= tok_begin) return CB_OK;
+                           int row_end, int tokens, cudaStream_t stream) {
+  if (row_end <= row_begin || tokens <= 0) return CB_OK;
   simt::Params p{};
   p.q = a.q;
   p.out = a.out;
@@ -34,8 +34,8 @@ cb_status launch_simt_rows(const cb_attention_args& a, const WsLayout& L, int ro
   p.block_tables = a.block_tables;
   p.row_begin = row_begin;
   p.row_end = row_end;
-  p.tok_begin = tok_begin;
-  p.tok_end = tok_end;
+  p.num_rows = a.num_reqs;
+  p.num_tokens = tokens;
   p.num_blocks = a.num_blocks;
   p.max_blocks_per_seq = a.max_blocks_per_seq;
   p.block_size = a.block_size;
@@ -44,7 +44,7 @@ cb_status launch_simt_rows(const cb_attention_args& a, const WsLayout& L, int ro
   p.scale_log2 = a.scale * 1.4426950408889634f;
   p.window = a.sliding_window;
   p.error_word = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(a.workspace) + L.header);
-  const int64_t warps = (int64_t)(tok_end - tok_begin) * a.num_q_heads;
+  const int64_t warps = (int64_t)tokens * a.num_q_heads;
   const int64_t blocks = (warps + 7) / 8;
   simt::rows_kernel<T, D><<<(unsigned)blocks, 256, 0, stream>>>(p);
   cudaError_t e = cudaGetLastError();
@@ -54,9 +54,9 @@ cb_status launch_simt_rows(const cb_attention_args& a, const WsLayout& L, int ro
 
 template <typename T>
 cb_status dispatch_simt(const cb_attention_args& a, const WsLayout& L, int row_begin, int row_end,
-                        int tok_begin, int tok_end, cudaStream_t s) {
-  if (a.head_dim == 64) return launch_simt_rows<T, 64>(a, L, row_begin, row_end, tok_begin, tok_end, s);
-  if (a.head_dim == 128) return launch_simt_rows<T, 128>(a, L, row_begin, row_end, tok_begin, tok_end, s);
+                        int tokens, cudaStream_t s) {
+  if (a.head_dim == 64) return launch_simt_rows<T, 64>(a, L, row_begin, row_end, tokens, s);
+  if (a.head_dim == 128) return launch_simt_rows<T, 128>(a, L, row_begin, row_end, tokens, s);
   return fail(CB_ERR_UNSUPPORTED, "head_dim %d not supported", a.head_dim);
 }
 
@@ -148,8 +148,10 @@ extern "C" cb_status cb_paged_attention(const cb_attention_args* args, cb_stream
     cb_status s = a.dtype == CB_DTYPE_BF16 ? cb::decode::dispatch_bf16(a, ds, ew, stream, after)
                                            : cb::decode::dispatch_f32(a, ds, ew, stream, after);
     if (s == CB_ERR_UNSUPPORTED) {
-      s = a.dtype == CB_DTYPE_BF16 ? cb::dispatch_simt<__nv_bfloat16>(a, L, 0, nd, 0, nd, stream)
-                                   : cb::dispatch_simt<float>(a, L, 0, nd, 0, nd, stream);
+      // (a decode row has one token, or none as padding)
+      const int tokens = nd < a.num_tokens ? nd : a.num_tokens;
+      s = a.dtype == CB_DTYPE_BF16 ? cb::dispatch_simt<__nv_bfloat16>(a, L, 0, nd, tokens, stream)
+                                   : cb::dispatch_simt<float>(a, L, 0, nd, tokens, stream);
     }
     return s;
   };
@@ -171,7 +173,6 @@ extern "C" cb_status cb_paged_attention(const cb_attention_args* args, cb_stream
     if (st != CB_OK) return st;
   }
   if (nd < a.num_reqs) {
-    // decode rows hold exactly one token each, so prefill tokens start at nd
     if (tc_prefill) {
       // the decode kernel just queued (if any) reads and writes nothing the
       // prefill rows use: let the prefill grid start on the SMs it frees
@@ -179,8 +180,8 @@ extern "C" cb_status cb_paged_attention(const cb_attention_args* args, cb_stream
       if (st != CB_ERR_UNSUPPORTED) return st;
     }
     st = a.dtype == CB_DTYPE_BF16
-             ? cb::dispatch_simt<__nv_bfloat16>(a, L, nd, a.num_reqs, nd, a.num_tokens, stream)
-             : cb::dispatch_simt<float>(a, L, nd, a.num_reqs, nd, a.num_tokens, stream);
+             ? cb::dispatch_simt<__nv_bfloat16>(a, L, nd, a.num_reqs, a.num_tokens, stream)
+             : cb::dispatch_simt<float>(a, L, nd, a.num_reqs, a.num_tokens, stream);
   }
   return st;
 }

@@ -28,8 +28,9 @@ struct Params {
   const int32_t* cu_seqlens_q;
   const int32_t* seq_lens;
   const int32_t* block_tables;
-  int32_t row_begin, row_end;   // rows handled
-  int32_t tok_begin, tok_end;   // = cu_seqlens_q[row_begin], cu_seqlens_q[row_end]
+  int32_t row_begin, row_end;   // rows handled; other rows' tokens are skipped
+  int32_t num_rows;             // rows of the call
+  int32_t num_tokens;           // tokens [0, num_tokens) are looked at
   int32_t num_blocks, max_blocks_per_seq, block_size;
   int32_t num_q_heads, num_kv_heads;
   float scale_log2;
@@ -61,23 +62,30 @@ __global__ void __launch_bounds__(256) rows_kernel(const Params p) {
   const int lane = threadIdx.x & 31;
   const int64_t wid = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
   const int Hq = p.num_q_heads;
-  const int64_t ntok = p.tok_end - p.tok_begin;
-  if (wid >= ntok * Hq) return;
-  const int t = p.tok_begin + (int)(wid / Hq);
+  if (blockIdx.x == 0) {
+    // rows whose queries end before they start
+    for (int i = p.row_begin + (int)threadIdx.x; i < p.row_end; i += (int)blockDim.x)
+      if (p.cu_seqlens_q[i + 1] < p.cu_seqlens_q[i]) set_error(p.error_word, CB_DEVERR_SEQ_RANGE);
+  }
+  if (wid >= (int64_t)p.num_tokens * Hq) return;
+  const int t = (int)(wid / Hq);
   const int h = (int)(wid % Hq);
-  // row of token t
-  int lo = p.row_begin, hi = p.row_end - 1;
+  // The last row whose queries start at or before t.  All rows are searched:
+  // with padding among the rows before row_begin, its tokens start anywhere
+  // up to their number, and tokens behind the last row belong to none.
+  int lo = 0, hi = p.num_rows - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
     if (p.cu_seqlens_q[mid] <= t) lo = mid; else hi = mid - 1;
   }
   const int r = lo;
   const int q0 = p.cu_seqlens_q[r];
-  const int q_len = p.cu_seqlens_q[r + 1] - q0;
+  const int q1 = p.cu_seqlens_q[r + 1], q_len = q1 - q0;
+  if (t < q0 || t >= q1 || r < p.row_begin || r >= p.row_end) return;
   const int L = p.seq_lens[r];
   const int bs = p.block_size;
   T* orow = static_cast<T*>(p.out) + ((int64_t)t * Hq + h) * D;
-  if (q_len < 1 || L < q_len || !row_length_fits(L, bs, p.max_blocks_per_seq)) {
+  if (L < q_len || !row_length_fits(L, bs, p.max_blocks_per_seq)) {
     if (lane == 0) set_error(p.error_word, CB_DEVERR_SEQ_RANGE);
     for (int e = lane; e < D; e += 32) store_elem<T>(orow + e, 0.f);
     return;
