@@ -162,7 +162,7 @@ extern "C" cb_status cb_paged_attention(const cb_attention_args* args, cb_stream
   // holds 16k keys or more), the prefill rows go first and the decode
   // kernel runs beside them on the idle SMs (programmatic dependent launch).
   if (nd > 0 && tc_prefill && a.max_seq_len >= 16384 &&
-      cb::prefill_ctas(a) + 16 <= cb::sm_count_current_device()) {
+      cb::prefill_busy_ctas(a) + 16 <= cb::sm_count_current_device()) {
     cb_status st = cb::launch_prefill_bf16(a, ew, ws + L.prefill, stream, false);
     if (st == CB_OK) return run_decode(cb::decode::After::kPrefill);
     if (st != CB_ERR_UNSUPPORTED) return st;

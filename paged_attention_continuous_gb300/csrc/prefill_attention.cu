@@ -620,7 +620,19 @@ int64_t prefill_ctas(const cb_attention_args& a) {
   const int G = a.num_q_heads / a.num_kv_heads;
   if (G <= 0 || G > kBM) return 0;
   const int tpp = 2 * (kBM / G);  // tokens per CTA (a pair of query tiles)
-  // every row's pairs: at most (prefill tokens) / tpp rounded up per row
+  // Rows of q_1, q_2, ... tokens have sum ceil(q_i / tpp) pairs, at most
+  // (sum q_i + rows (tpp - 1)) / tpp.  Decode rows may be padding without
+  // tokens, so all the call's tokens may be theirs.
+  const int64_t rows = a.num_reqs - a.num_decodes;
+  const int64_t pairs = rows > 0 ? ((int64_t)a.num_tokens + rows * (tpp - 1)) / tpp : 0;
+  return pairs * a.num_kv_heads;
+}
+
+int64_t prefill_busy_ctas(const cb_attention_args& a) {
+  using namespace prefill;
+  const int G = a.num_q_heads / a.num_kv_heads;
+  if (G <= 0 || G > kBM) return 0;
+  const int tpp = 2 * (kBM / G);
   const int64_t pairs = ((int64_t)a.num_tokens - a.num_decodes + tpp - 1) / tpp +
                         (a.num_reqs - a.num_decodes);
   return pairs > 0 ? pairs * a.num_kv_heads : 0;

@@ -22,6 +22,10 @@ size_t prefill_workspace_bytes(int64_t Hq, int64_t Hkv, int64_t D);
 // 0 without prefill rows).
 int64_t prefill_ctas(const cb_attention_args& a);
 
+// About as many of those as find work when every decode row has its token
+// (for choosing an order of launches: with padding among them it is low).
+int64_t prefill_busy_ctas(const cb_attention_args& a);
+
 // Launch the prefill-chunk kernel over rows [num_decodes, num_reqs) (bf16,
 // head_dim 128).  Returns CB_ERR_UNSUPPORTED if it cannot take this call.
 // overlap_previous: the kernel queued just before on `stream` is the decode

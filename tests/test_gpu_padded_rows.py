@@ -1,6 +1,7 @@
 """cb_paged_attention (16/32-bit caches) where decode rows, prefill rows and
-tokens are padding: a chunk's tokens then start before num_decodes, and
-tokens lie behind the last row.  Every real row is as in the call without padding, bit for bit; the rest
+tokens are padding: a chunk's tokens then start before num_decodes, the chunk
+has more tokens than num_tokens - num_decodes, and tokens lie behind the last
+row.  Every real row is as in the call without padding, bit for bit; the rest
 of the output stays."""
 import numpy as np
 import pytest
@@ -116,3 +117,19 @@ def test_graph_runner_of_the_row_kernel(hq, hkv, D, dtype):
         assert torch.equal(graph.out_buf[0][:T], want)
         sched.step_done()
     assert mixed and eager.workspace.read_errors() == 0 and graph.workspace.read_errors() == 0
+
+
+@pytest.mark.parametrize("nd,chunks,pad,extra", [
+    (129, [383], 127, 0),         # 129 decodes in a bucket of 256, 512 tokens
+    (0, [512], 255, 0),           # tables of 256 rows, one of them busy
+    (3, [200, 130], 300, 5),
+])
+def test_chunks_behind_many_padded_decode_rows(nd, chunks, pad, extra):
+    """bf16, 128 dims: the prefill grid covers every query tile."""
+    rows = [(20 + 7 * i % 90, 1) for i in range(nd)] + [(m + 33, m) for m in chunks]
+    c = Call(rows, 4, 1, 128, "bf16", seed=nd)
+    plain = c.run(list(range(len(rows))), nd)
+    c.near_oracle(plain)
+    order = list(range(nd)) + [None] * pad + list(range(nd, len(rows)))
+    extra = max(extra, len(order) - c.T)
+    assert torch.equal(c.run(order, nd + pad, extra), plain)
