@@ -420,7 +420,8 @@ typedef struct cb_attention_args {
   const int32_t* block_tables;  /* device [num_reqs][max_blocks_per_seq] */
   int32_t num_reqs;
   int32_t num_decodes;          /* rows [0, num_decodes) are decodes */
-  int32_t num_tokens;
+  int32_t num_tokens;           /* rows of q and out; fewer than num_reqs
+                                   where enough rows are padding */
   int32_t max_q_len;            /* host bound on rows' query length */
   int32_t max_seq_len;          /* host bound on seq_lens */
   int32_t num_blocks;           /* pool size (block ids are range-checked) */

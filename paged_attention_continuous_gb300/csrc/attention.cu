@@ -69,7 +69,6 @@ cb_status check_attention(const cb_attention_args& a) {
   if (!a.q || !a.out || !a.k_cache || !a.v_cache || !a.cu_seqlens_q || !a.seq_lens ||
       !a.block_tables || !a.workspace)
     return fail(CB_ERR_INVALID_ARG, "NULL pointer argument");
-  if (a.num_tokens < a.num_reqs) return fail(CB_ERR_INVALID_ARG, "num_tokens < num_reqs");
   if (a.num_q_heads <= 0 || a.num_kv_heads <= 0 || a.num_q_heads % a.num_kv_heads != 0)
     return fail(CB_ERR_INVALID_ARG, "num_q_heads must be a positive multiple of num_kv_heads");
   if (a.num_kv_heads > kMaxKvHeads)
