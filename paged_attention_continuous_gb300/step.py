@@ -322,18 +322,26 @@ class DeviceTables:
         """``max_q_len`` / ``max_seq_len``: host bounds on the rows' query and
         sequence lengths (default: what the tables and tokens allow);
         ``num_tokens``: how many tokens the step has room for (default: all
-        of max_tokens)."""
+        of max_tokens; q, k and v have that many rows, and may be fewer than
+        max_reqs).  What the attention would refuse is refused here, before
+        the tables move on."""
         R, W = self.block_tables.shape
         T = self.max_tokens if num_tokens is None else int(num_tokens)
-        longest = W * self.block_size
+        if not 0 <= T <= self.max_tokens:
+            raise ValueError(f"num_tokens must lie in [0, {self.max_tokens}]")
+        if not 0 <= num_decodes <= R:
+            raise ValueError(f"num_decodes must lie in [0, {R}]")
+        longest = W * self.block_size if max_seq_len is None else int(max_seq_len)
+        if not 1 <= longest <= W * self.block_size:
+            raise ValueError(f"max_seq_len must lie in [1, {W * self.block_size}]")
+        most = max(1, 1 if num_decodes == R else min(T, longest)) if max_q_len is None else int(max_q_len)
+        if not 1 <= most <= longest:
+            raise ValueError("max_q_len must lie in [1, max_seq_len]")
         step_tables(q_lens, self.cached_lens, self.block_tables, self.free_ring, self.free_state,
                     cu_seqlens_q=self.cu_seqlens_q, seq_lens=self.seq_lens,
                     slot_mapping=self.slot_mapping[:T], positions=self.positions[:T],
                     block_size=self.block_size, error_word=self.error_word)
-        most = 1 if num_decodes == R else min(T, longest)
-        return DeviceStep(R, T, num_decodes, most if max_q_len is None else int(max_q_len),
-                          longest if max_seq_len is None else int(max_seq_len),
-                          self.cu_seqlens_q, self.seq_lens, self.block_tables,
+        return DeviceStep(R, T, num_decodes, most, longest, self.cu_seqlens_q, self.seq_lens, self.block_tables,
                           self.slot_mapping[:T], 0, self.positions[:T])
 
     def trim(self, keep_lens) -> None:
