@@ -435,6 +435,18 @@ def _stream_ptr(stream) -> int:
     return int(stream.cuda_stream)
 
 
+def _new_like(t, stream):
+    """An uninitialised contiguous tensor like t, to be written on ``stream``
+    (None: the current one).  It belongs to that stream, as if the caller had
+    allocated it there: memory of the current stream may still be in use by
+    work queued on it, or be handed out again while ``stream`` writes."""
+    torch = _torch()
+    if stream is None:
+        return torch.empty_like(t, memory_format=torch.contiguous_format)
+    with torch.cuda.stream(stream):
+        return torch.empty_like(t, memory_format=torch.contiguous_format)
+
+
 def _need_cuda(*ts):
     for t in ts:
         if not t.is_cuda:
@@ -526,7 +538,8 @@ class Workspace:
         torch = _torch()
         self.nbytes = workspace_size(max_reqs, num_q_heads, num_kv_heads, head_dim)
         self.max_reqs = max_reqs
-        self.buf = torch.empty(self.nbytes + 256, dtype=torch.uint8, device=device)
+        with torch.cuda.stream(stream):      # (None: the current one)
+            self.buf = torch.empty(self.nbytes + 256, dtype=torch.uint8, device=device)
         off = (-self.buf.data_ptr()) % 256
         self.ptr = self.buf.data_ptr() + off
         _check(_lib.cb_attention_workspace_init(self.ptr, self.nbytes, _stream_ptr(stream)))
@@ -552,10 +565,9 @@ def paged_attention(q, k_cache, v_cache, cu_seqlens_q, seq_lens, block_tables, *
     sliding-window layer; ``after_append``: the launch just before on the
     stream was this step's kv_append (the decode kernel then overlaps its
     end).  Returns out [T, Hq, D]."""
-    torch = _torch()
     _need_cuda(q, k_cache, v_cache, cu_seqlens_q, seq_lens, block_tables)
     if out is None:
-        out = torch.empty_like(q)
+        out = _new_like(q, stream)
     T, hq, d = q.shape
     nb, hkv, bs, _ = k_cache.shape
     R = seq_lens.shape[0]
@@ -733,7 +745,6 @@ def rope(q, k, positions, plan: RopePlan, *, q_out=None, k_out=None, inverse: bo
     ``positions`` int32 [T]; returns (q_out, k_out).  An output may be its
     input.  ``inverse`` rotates back, which also turns gradients of the
     outputs into gradients of the inputs."""
-    torch = _torch()
     first = q if q is not None else k
     if first is None:
         raise ValueError("neither q nor k is given")
@@ -742,11 +753,11 @@ def rope(q, k, positions, plan: RopePlan, *, q_out=None, k_out=None, inverse: bo
     qa = ka = (0, 0, 0, 0, 0)
     if q is not None:
         if q_out is None:
-            q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
+            q_out = _new_like(q, stream)
         qa = _rope_rows("q", q, q_out, dev, T, d, dtype)
     if k is not None:
         if k_out is None:
-            k_out = torch.empty_like(k, memory_format=torch.contiguous_format)
+            k_out = _new_like(k, stream)
         ka = _rope_rows("k", k, k_out, dev, T, d, dtype)
     pos, = _i32(dev, (("positions", positions, T),))
     a = _pack_rope(plan._at, pos, T, qa[4], ka[4], _dtype_code(first), 1 if inverse else 0, *qa[:4], *ka[:4])
@@ -815,7 +826,7 @@ def kv_append_q8(k_new, v_new, slot_mapping, k_cache, v_cache, k_scales, v_scale
         pos, = _i32(dev, (("positions", positions, T),))
         if q is not None:
             if q_out is None:
-                q_out = _torch().empty_like(q)
+                q_out = _new_like(q, stream)
             hq = q.shape[1]
             qp = _rows3("q", q, dev, dtype, T, None, d)
             op = _rows3("q_out", q_out, dev, dtype, T, hq, d)
@@ -836,7 +847,7 @@ def paged_attention_q8(q, k_cache, v_cache, k_scales, v_scales, cu_seqlens_q, se
     dev, st = _launch_on(q, stream)
     (nb, hkv, bs, d), ss, kc, vc, ks, vs = _q8(dev, k_cache, v_cache, k_scales, v_scales)
     if out is None:
-        out = _torch().empty_like(q)
+        out = _new_like(q, stream)
     T, hq = q.shape[0], q.shape[1]
     qp = _rows3("q", q, dev, q.dtype, T, hq, d)
     op = _rows3("out", out, dev, q.dtype, T, hq, d)
