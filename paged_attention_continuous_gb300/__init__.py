@@ -739,12 +739,59 @@ def _rope_rows(name, x, out, dev, T, d, dtype):
     return x.data_ptr(), out.data_ptr(), strides[0], strides[1], H
 
 
+_rope_class = None
+
+
+def _rope_function():
+    """The autograd function of rope (made at its first use, as torch is
+    imported then)."""
+    global _rope_class
+    if _rope_class is not None:
+        return _rope_class
+    torch = _torch()
+
+    class Rope(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, q, k, positions, plan, inverse):
+            out = rope(q, k, positions, plan, inverse=inverse)     # (nothing is recorded in here)
+            # a copy: the caller's positions are those of its next step by then
+            ctx.save_for_backward(positions.clone())
+            ctx.plan, ctx.inverse = plan, inverse
+            ctx.set_materialize_grads(False)
+            ctx.mark_non_differentiable(*(o for o, need in zip(out, ctx.needs_input_grad) if o is not None and not need))
+            return out
+
+        @staticmethod
+        def backward(ctx, gq, gk):
+            # (contiguous: a gradient may be one number expanded to all elements)
+            gq, gk = (g.contiguous() if g is not None and need else None
+                      for g, need in zip((gq, gk), ctx.needs_input_grad))
+            if gq is None and gk is None:
+                return None, None, None, None, None
+            positions, = ctx.saved_tensors
+            return *rope(gq, gk, positions, ctx.plan, inverse=not ctx.inverse), None, None, None
+
+    _rope_class = Rope
+    return Rope
+
+
 def rope(q, k, positions, plan: RopePlan, *, q_out=None, k_out=None, inverse: bool = False,
          stream=None):
     """cb_rope: rotate q [T, Hq, D] and k [T, Hkv, D] (either may be None) by
     ``positions`` int32 [T]; returns (q_out, k_out).  An output may be its
-    input.  ``inverse`` rotates back, which also turns gradients of the
-    outputs into gradients of the inputs."""
+    input.  ``inverse`` negates the angles: the transpose, which turns
+    gradients of the outputs into gradients of the inputs (and turns rows back
+    where the plan's amplitude m is 1; otherwise there and back gives m^2
+    times the row).
+
+    Differentiable: where q or k requires a gradient and autograd records,
+    the outputs carry it (also of second order), and may not be given."""
+    if (q is not None and q.requires_grad or k is not None and k.requires_grad) \
+            and _torch().is_grad_enabled():
+        if q_out is not None or k_out is not None:
+            raise ValueError("rope: outputs cannot be given where a gradient is recorded")
+        with _torch().cuda.stream(stream):      # (None: the current one); the backward runs there too
+            return _rope_function().apply(q, k, positions, plan, inverse)
     first = q if q is not None else k
     if first is None:
         raise ValueError("neither q nor k is given")
@@ -762,6 +809,10 @@ def rope(q, k, positions, plan: RopePlan, *, q_out=None, k_out=None, inverse: bo
     pos, = _i32(dev, (("positions", positions, T),))
     a = _pack_rope(plan._at, pos, T, qa[4], ka[4], _dtype_code(first), 1 if inverse else 0, *qa[:4], *ka[:4])
     _check(_lib.cb_rope(a, st))
+    # autograd is told of inputs that were overwritten (as torch's in-place
+    # operations do; about 1 us of host time, so not of other outputs)
+    if q is not None and qa[0] == qa[1] or k is not None and ka[0] == ka[1]:
+        _torch().autograd.graph.increment_version([t for t in (q_out, k_out) if t is not None])
     return q_out, k_out
 
 
@@ -811,7 +862,8 @@ def kv_append_q8(k_new, v_new, slot_mapping, k_cache, v_cache, k_scales, v_scale
     ``k_cache``/``v_cache`` float8_e4m3fn [num_blocks, Hkv, 16, D],
     ``k_scales``/``v_scales`` uint8 [num_blocks, Hkv].  With ``rope`` (and
     ``positions`` int32 [T]) k is rotated first, and ``q`` [T, Hq, D]
-    (optional) into ``q_out``, which is returned."""
+    (optional) into ``q_out``, which is returned.  Nothing is differentiable
+    here (``rope`` is)."""
     dev, st = _launch_on(k_cache, stream)
     (nb, hkv, bs, d), ss, kc, vc, ks, vs = _q8(dev, k_cache, v_cache, k_scales, v_scales)
     T, dtype = slot_mapping.numel(), k_new.dtype
@@ -835,6 +887,8 @@ def kv_append_q8(k_new, v_new, slot_mapping, k_cache, v_cache, k_scales, v_scale
     a = _pack_append(kp, vp, slots, T, _dtype_code(k_new), kc, vc, ks, vs, ss, nb, hkv, d, bs,
                      plan, pos, qp, op, hq, _error_ptr(error_word, dev))
     _check(_lib.cb_kv_append_q8(a, st))
+    if qp and qp == op:        # q was overwritten: autograd is told
+        _torch().autograd.graph.increment_version(q_out)
     return q_out if q is not None else None
 
 
