@@ -568,10 +568,11 @@ cb_status cb_trim_tables(const cb_tables* tables, const int32_t* keep_lens, cb_s
  *   CB_ROPE_LINEAR  f_i / factor
  *   CB_ROPE_NTK     f_i of the base base * factor^(rot_dim / (rot_dim - 2))
  *   CB_ROPE_PARTS   f_i (k_i + (1 - k_i) / factor), k_i = 1 - clamp((i - lo)
- *                   / (hi - lo), 0, 1), lo = floor(at(beta_fast)) >= 0, hi =
- *                   ceil(at(beta_slow)) <= rot_dim / 2 - 1 (lo + 0.001 if
- *                   they are equal), at(n) = rot_dim ln(original_positions /
- *                   (2 pi n)) / (2 ln base); m = 0.1 ln(factor) + 1
+ *                   / (hi - lo), 0, 1), lo = max(floor(at(beta_fast)), 0), hi =
+ *                   min(ceil(at(beta_slow)), rot_dim - 1) (lo + 0.001 if
+ *                   they are equal; hi < lo is refused), at(n) = rot_dim
+ *                   ln(original_positions / (2 pi n)) / (2 ln base); m =
+ *                   0.1 ln(factor) + 1
  *   CB_ROPE_BANDS   the same with k_i = clamp((n_i - low_freq_factor) /
  *                   (high_freq_factor - low_freq_factor), 0, 1), n_i =
  *                   original_positions f_i / (2 pi); m = 1

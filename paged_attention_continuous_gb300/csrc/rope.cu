@@ -166,7 +166,13 @@ extern "C" cb_status cb_rope_plan_init(const cb_rope_config* config, cb_rope_pla
       return rot * std::log(c.original_positions / (two_pi * n)) / (2.0 * std::log(base));
     };
     lo = std::fmax(std::floor(at(c.beta_fast)), 0.0);
-    hi = std::fmin(std::ceil(at(c.beta_slow)), rot / 2 - 1);
+    // (rot - 1, not the last pair's rot / 2 - 1: a ramp that reaches past the
+    // pairs keeps its slope)
+    hi = std::fmin(std::ceil(at(c.beta_slow)), rot - 1);
+    if (hi < lo)
+      return fail(CB_ERR_INVALID_ARG,
+                  "cb_rope_plan_init: the ramp would end (%.0f) before it starts (%.0f): original_positions "
+                  "does not go with base and betas", hi, lo);
     if (hi == lo) hi = lo + 0.001;
   }
   double amplitude = parts && c.factor > 1.0 ? 0.1 * std::log(c.factor) + 1.0 : 1.0;
