@@ -707,9 +707,14 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       }
       // zeros, or a row that is not finite (nor are its scores): factor 1
       const int k = amax > 0.f && amax <= 3.402823466e38f ? max((int)(__float_as_uint(amax) >> 23) - 127, -110) : 14;
-      const float up = p.scale_log2 == 0.f ? 0.f : p.scale_log2 < 0.f ? -q8::exp2i(14 - k) : q8::exp2i(14 - k);
-      // (never so small that times a block's scale it is 0: a masked score is -inf)
-      hs = p.scale_log2 == 0.f ? 1.f : fmaxf(fabsf(p.scale_log2) * q8::exp2i(k - 14), q8::exp2i(-80));
+      // The row's factor is never so small that times a block's scale it is 0
+      // (a masked score is -inf): below 2^-80 it stays there and what is
+      // missing goes into Q, whose halves then lose bits of scores that are
+      // under 2^-9 at any scale of the blocks.
+      const float mag = fabsf(p.scale_log2), factor = mag * q8::exp2i(k - 14);
+      const bool tiny = factor < q8::exp2i(-80);
+      hs = mag == 0.f ? 1.f : tiny ? q8::exp2i(-80) : factor;
+      const float up = copysignf(mag == 0.f ? 0.f : tiny ? mag * q8::exp2i(80) : q8::exp2i(14 - k), p.scale_log2);
 #pragma unroll
       for (int i = 0; i < D / 8; ++i) {
         float x[8];
