@@ -353,9 +353,12 @@ cb_status launch(Kernel kernel, const Params& p, int64_t items, std::atomic<uint
   cb_status st = ensure_smem_attr(reinterpret_cast<const void*>(kernel), rows_bytes(kMaxRows), attr_set);
   if (st != CB_OK) return st;
   cudaLaunchConfig_t cfg{};
-  // one CTA while its threads hold every token and row at once, else the
-  // portable cluster size (step and trim of 64 rows, 64 tokens: 9.6 us, 9.8
-  // with eight; 80 rows, 10k tokens: 10.5 us with eight, 16.1 with one)
+  // one CTA while its threads hold every token and row at once (and every page
+  // that a trim may give back, at one to a thread), else the portable cluster
+  // size (step and trim of 64 rows, 64 tokens: 9.6 us, 9.8 with a cluster for
+  // both; 80 rows, 10k tokens: 10.5 us with eight, 16.1 with one; a trim alone
+  // that gives back 64 pages 9.3 us either way, 4096 9.3 and 13.5, 131k 25.7
+  // and 148.6)
   const unsigned ctas = items <= kThreads * 4 ? 1 : 8;
   cfg.gridDim = dim3(ctas, 1, 1);
   cfg.blockDim = dim3(kThreads, 1, 1);
@@ -414,6 +417,8 @@ extern "C" cb_status cb_trim_tables(const cb_tables* tables, const int32_t* keep
   if (st != CB_OK) return st;
   const Params p = params_of(*tables, keep_lens);
   static std::atomic<uint8_t> attr_set[cb::kMaxDevices];
-  return launch(trim_kernel, p, tables->num_rows * 4ll, attr_set, (cudaStream_t)stream,
-                "cb_trim_tables");
+  const int64_t entries = (int64_t)tables->num_rows * tables->max_blocks_per_seq;
+  const int64_t pages = entries < tables->num_blocks ? entries : tables->num_blocks;
+  const int64_t items = (pages > tables->num_rows ? pages : tables->num_rows) * 4;
+  return launch(trim_kernel, p, items, attr_set, (cudaStream_t)stream, "cb_trim_tables");
 }
