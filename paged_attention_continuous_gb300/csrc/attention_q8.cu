@@ -31,7 +31,7 @@ struct RowsParams {
   const int32_t* seq_lens;
   const int32_t* block_tables;
   int32_t row_begin, row_end;   // rows handled; others' tokens are skipped
-  int32_t num_rows, num_tokens;
+  int32_t num_rows, num_decodes, num_tokens;
   int32_t num_blocks, max_blocks_per_seq;
   int32_t num_q_heads, num_kv_heads;
   float scale_log2;
@@ -47,6 +47,19 @@ __global__ void __launch_bounds__(256) rows_kernel(const RowsParams p) {
   const int lane = threadIdx.x & 31;
   const int64_t wid = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
   const int Hq = p.num_q_heads, Hkv = p.num_kv_heads;
+  if (blockIdx.x == 0) {
+    // rows that are no rows: the other kernels' checks of lengths and queries
+    for (int r = p.row_begin + (int)threadIdx.x; r < p.row_end; r += (int)blockDim.x) {
+      const int q0 = p.cu_seqlens_q[r], q_len = p.cu_seqlens_q[r + 1] - q0, L = p.seq_lens[r];
+      if (q_len == 0 && L == 0) continue;  // padding
+      if (r < p.num_decodes) {
+        if (q_len != 1 || !row_tokens_fit(q0, 1, p.num_tokens)) set_error(p.error_word, CB_DEVERR_DECODE_QLEN);
+        if (!row_length_fits(L, kPage, p.max_blocks_per_seq)) set_error(p.error_word, CB_DEVERR_SEQ_RANGE);
+      } else if (q_len < 1 || !row_tokens_fit(q0, q_len, p.num_tokens)) {
+        set_error(p.error_word, CB_DEVERR_SEQ_RANGE);
+      }
+    }
+  }
   if (wid >= (int64_t)p.num_tokens * Hq) return;
   const int t = (int)(wid / Hq), h = (int)(wid % Hq);
   // the last row whose queries start at or before t
@@ -58,6 +71,7 @@ __global__ void __launch_bounds__(256) rows_kernel(const RowsParams p) {
   const int r = lo, q0 = p.cu_seqlens_q[r], q1 = p.cu_seqlens_q[r + 1];
   if (t < q0 || t >= q1 || r < p.row_begin || r >= p.row_end) return;
   const int L = p.seq_lens[r], q_len = q1 - q0;
+  if ((r < p.num_decodes && q_len != 1) || !row_tokens_fit(q0, q_len, p.num_tokens)) return;  // flagged above
   if (L < q_len || !row_length_fits(L, kPage, p.max_blocks_per_seq)) {
     if (lane == 0) set_error(p.error_word, CB_DEVERR_SEQ_RANGE);
     return;
@@ -198,6 +212,7 @@ extern "C" cb_status cb_paged_attention_q8(const cb_attention_args* args, const 
   p.row_begin = decodes_left ? 0 : nd;
   p.row_end = prefills_left ? a.num_reqs : nd;
   p.num_rows = a.num_reqs;
+  p.num_decodes = nd;
   p.num_tokens = a.num_tokens;
   p.num_blocks = a.num_blocks;
   p.max_blocks_per_seq = a.max_blocks_per_seq;
