@@ -19,6 +19,11 @@ template <typename T, int D, int kNT>
 cb_status launch(const cb_attention_args& a, const uint8_t* k_scales, const uint8_t* v_scales,
                  int64_t scale_stride, int parts, int part_heads, const decode::Scratch& s,
                  uint32_t* error_word, cudaStream_t stream, decode::After after) {
+  // Two stages of two pages to a warp keep 128 KB of an SM in flight with 128
+  // dims, 64 KB with 64.  More change little: 64 requests of up to 4k tokens,
+  // 128 dims 63.3 us with two and 64.0 with three, 64 dims 54.0 and 53.6 with
+  // four; 128 of up to 32k tokens 636 and 633, 64 dims 513 and 507; float32
+  // queries 72.4 and 73.1, 707 and 712.
   constexpr int kStages = 2;
   using Lay = Layout<D, kStages>;
   auto kern = decode_kernel<T, D, kNT, kStages>;

@@ -112,9 +112,12 @@ __device__ __forceinline__ void store_codes(uint8_t* dst, const float (&x)[N], f
 
 // CTAs an SM should hold: four, where the registers of a run allow it (the
 // 6.9k tokens with q turned 35.9 us with four, 37.9 with three, before runs
-// were dealt to warps)
+// were dealt to warps).  float32 runs take twice the registers of bfloat16
+// ones.  The 6.9k tokens in float32 with 1 / 2 / 3 CTAs: 128 dims 17.5 / 17.7
+// / 18.0 us, with q and k turned 62.1 / 62.0 / 56.8; 64 dims 9.8 / 9.7 / 9.7,
+// and 8.3 with four, turned 36.8 / 36.8 / 30.5.
 template <typename T, int D, int kRope>
-constexpr int resident() { return sizeof(T) == 2 ? 4 : D == 128 ? 2 : kRope == kNoRope ? 4 : 3; }
+constexpr int resident() { return sizeof(T) == 2 ? 4 : kRope != kNoRope ? 3 : D == 64 ? 4 : 2; }
 
 template <typename T, int D, int kRope>
 __global__ void __launch_bounds__(kThreads, resident<T, D, kRope>())
