@@ -68,37 +68,6 @@ struct Params {
   uint32_t* error_word;
 };
 
-// Rotates q: tokens t0 ... of one CTA, a unit of the rows to a thread.
-template <typename T, int kRope>
-__device__ __forceinline__ void rotate_q(const Params& p, int t0, int tokens, float2* cs) {
-  constexpr int N = Vec<T>::kN;
-  constexpr int kAhead = 2;  // 64 bytes of loads in flight per thread
-  const uint32_t items = (uint32_t)tokens * p.q_rows.heads * p.q_rows.units;
-  rope::Unit<T, N> w[kAhead];
-  uint32_t n = threadIdx.x;
-#pragma unroll
-  for (int i = 0; i < kAhead; ++i)
-    if (n + i * kThreads < items) rope::load_unit<T, N, kRope == kHalf>(p.q_rows, t0, n + i * kThreads, w[i]);
-  const int pairs = p.plan.rot_dim / 2;
-  for (int i = threadIdx.x; i < tokens * pairs; i += kThreads) {
-    const int tl = i / pairs, pair = i - tl * pairs;
-    cs[tl * pairs + rope::angle_at<N, kRope == kHalf>(pair, pairs)] =
-        rope::turn_of(p.plan.turns[pair], p.positions[t0 + tl], p.plan.amplitude, false);
-  }
-  __syncthreads();
-  while (true) {
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i)
-      if (n + i * kThreads < items)
-        rope::store_unit<T, N, kRope == kHalf>(cs, pairs / rope::unit_pairs<N, kRope == kHalf>(), w[i]);
-    n += kAhead * kThreads;
-    if (n >= items) break;
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i)
-      if (n + i * kThreads < items) rope::load_unit<T, N, kRope == kHalf>(p.q_rows, t0, n + i * kThreads, w[i]);
-  }
-}
-
 // The codes of N values, in one store.
 template <int N>
 __device__ __forceinline__ void store_codes(uint8_t* dst, const float (&x)[N], float f) {
@@ -137,7 +106,9 @@ __global__ void __launch_bounds__(kThreads, resident<T, D, kRope>())
   if constexpr (kRope != kNoRope) {
     if ((int)blockIdx.y >= 2 * p.kv_ctas) {
       const int q0 = t0 + ((int)blockIdx.y - 2 * p.kv_ctas) * p.q_tokens;
-      if (q0 < p.num_tokens) rotate_q<T, kRope>(p, q0, min(p.q_tokens, p.num_tokens - q0), cs);
+      if (q0 < p.num_tokens)
+        rope::rotate_rows<T, Vec<T>::kN, kRope == kHalf, kThreads>(
+            p.q_rows, p.plan, p.positions, q0, min(p.q_tokens, p.num_tokens - q0), false, cs);
       return;
     }
   }

@@ -42,31 +42,7 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
   extern __shared__ float2 cs[];  // [tokens_per_cta][rot_dim / 2]
   const int t0 = (int)blockIdx.x * p.tokens_per_cta;
   const int tokens = min(p.tokens_per_cta, p.num_tokens - t0);
-  const uint32_t items = (uint32_t)tokens * p.rows.heads * p.rows.units;
-  constexpr int kAhead = N == 1 ? 1 : 2;  // 64 bytes of loads in flight per thread
-  Unit<T, N> w[kAhead];
-  uint32_t n = threadIdx.x;
-#pragma unroll
-  for (int i = 0; i < kAhead; ++i)
-    if (n + i * kThreads < items) load_unit<T, N, kHalf>(p.rows, t0, n + i * kThreads, w[i]);
-  const int pairs = p.plan.rot_dim / 2;
-  for (int i = threadIdx.x; i < tokens * pairs; i += kThreads) {
-    const int tl = i / pairs;
-    const int pair = i - tl * pairs;
-    cs[tl * pairs + angle_at<N, kHalf>(pair, pairs)] =
-        turn_of(p.plan.turns[pair], p.positions[t0 + tl], p.plan.amplitude, p.inverse != 0);
-  }
-  __syncthreads();
-  while (true) {
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i)
-      if (n + i * kThreads < items) store_unit<T, N, kHalf>(cs, pairs / unit_pairs<N, kHalf>(), w[i]);
-    n += kAhead * kThreads;
-    if (n >= items) break;
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i)
-      if (n + i * kThreads < items) load_unit<T, N, kHalf>(p.rows, t0, n + i * kThreads, w[i]);
-  }
+  rotate_rows<T, N, kHalf, kThreads>(p.rows, p.plan, p.positions, t0, tokens, p.inverse != 0, cs);
 }
 
 template <typename T, int N, bool kHalf>

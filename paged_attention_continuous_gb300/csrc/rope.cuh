@@ -207,5 +207,38 @@ __device__ __forceinline__ void store_unit(const float2* cs, int stride, const U
   }
 }
 
+// Rotates the rows of tokens t0 .. t0 + tokens: all kThreads threads of a CTA,
+// a unit to a thread at a time.  The first units are loaded before the angles
+// (cs: tokens * rot_dim / 2 of them, in shared memory), so that their
+// latencies overlap.
+template <typename T, int N, bool kHalf, int kThreads>
+__device__ __forceinline__ void rotate_rows(const Rows& rows, const cb_rope_plan& plan, const int32_t* positions,
+                                            int t0, int tokens, bool inverse, float2* cs) {
+  constexpr int kAhead = N == 1 ? 1 : 2;  // 64 bytes of loads in flight per thread
+  const uint32_t items = (uint32_t)tokens * rows.heads * rows.units;
+  Unit<T, N> w[kAhead];
+  uint32_t n = threadIdx.x;
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i)
+    if (n + i * kThreads < items) load_unit<T, N, kHalf>(rows, t0, n + i * kThreads, w[i]);
+  const int pairs = plan.rot_dim / 2;
+  for (int i = threadIdx.x; i < tokens * pairs; i += kThreads) {
+    const int tl = i / pairs, pair = i - tl * pairs;
+    cs[tl * pairs + angle_at<N, kHalf>(pair, pairs)] =
+        turn_of(plan.turns[pair], positions[t0 + tl], plan.amplitude, inverse);
+  }
+  __syncthreads();
+  while (true) {
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+      if (n + i * kThreads < items) store_unit<T, N, kHalf>(cs, pairs / unit_pairs<N, kHalf>(), w[i]);
+    n += kAhead * kThreads;
+    if (n >= items) break;
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+      if (n + i * kThreads < items) load_unit<T, N, kHalf>(rows, t0, n + i * kThreads, w[i]);
+  }
+}
+
 }  // namespace rope
 }  // namespace cb
