@@ -884,6 +884,8 @@ def kv_append_q8(k_new, v_new, slot_mapping, k_cache, v_cache, k_scales, v_scale
             op = _rows3("q_out", q_out, dev, dtype, T, hq, d)
     elif q is not None or positions is not None:
         raise ValueError("q and positions go with rope")
+    if q is None and q_out is not None:
+        raise ValueError("q_out goes with q")
     a = _pack_append(kp, vp, slots, T, _dtype_code(k_new), kc, vc, ks, vs, ss, nb, hkv, d, bs,
                      plan, pos, qp, op, hq, _error_ptr(error_word, dev))
     _check(_lib.cb_kv_append_q8(a, st))
