@@ -414,7 +414,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             // sequence: zero them (both 64-dim halves) before P.V reads them
             // (both issuers write the same zeros)
             uint8_t* vt = smem + SmemLayout::v + sp * kTileBytes;
-            const int r0 = L - jp * kBN, r1 = (npages - jp * (kBN / kPage)) * kPage;
+            const int r0 = L - jp * kBN, r1 = (int)(((uint32_t)L + kPage - 1u) / kPage * kPage) - jp * kBN;
             for (int rw = r0; rw < r1; ++rw)
               for (int c = 0; c < 8; ++c) {
                 *reinterpret_cast<uint4*>(vt + rw * 128 + c * 16) = make_uint4(0, 0, 0, 0);

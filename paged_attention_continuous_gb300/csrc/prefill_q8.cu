@@ -914,11 +914,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
           }
           __syncwarp();  // before the next dims take its place
         };
-        const bool any_nan = *reinterpret_cast<volatile int32_t*>(&B->nan_any) != 0;
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
-          const uint32_t nan = any_nan ? nan_dims<D>(p, VB, g, 32 * c, pos, key_row) : 0u;
-          __syncwarp();                           // (rows look at numbers of keys of their own)
           float o[32];
           tc::tmem_ld32_sync(trow + colO + 32 * c, o);
           if (kF32 && nt > 1) {
@@ -929,11 +926,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
           }
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e] *= inv;
-          if (any_nan) {
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (nan >> e & 1) o[e] = __int_as_float(0x7fffffff);
-          }
           if (parted) {
             // 32 dims of this split's part, in float32, row by row
             store_part(turn, c, o);
@@ -956,6 +948,21 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
           const uint4 v = *reinterpret_cast<const uint4*>(turn + (rr * kChunks + (chunk ^ (rr & 7))) * 16);
           const int64_t at = row_at((warp & 3) * 32 + rr);
           if (at >= 0) *reinterpret_cast<uint4*>(static_cast<T*>(p.out) + at) = v;
+        }
+        // NaN over the rows' outputs where it belongs (apart from the rest, which
+        // every call runs)
+        if (*reinterpret_cast<volatile int32_t*>(&B->nan_any) != 0) {
+          __syncwarp();                             // the rows are written
+          const int64_t at = valid ? (parted ? slot_of(row) : (int64_t)(q0 + tok)) * p.num_q_heads + head_of(row) : -1;
+#pragma unroll 1
+          for (int c = 0; c < D / 32 && valid; ++c) {
+            uint32_t nan = nan_dims<D>(p, VB, g, 32 * c, pos, key_row);
+            for (; nan != 0; nan &= nan - 1) {
+              const int64_t d = at * D + 32 * c + __ffs(nan) - 1;
+              if (parted) p.part_acc[d] = __int_as_float(0x7fffffff);
+              else rope::from_float(static_cast<T*>(p.out) + d, __int_as_float(0x7fffffff));
+            }
+          }
         }
       }
     }

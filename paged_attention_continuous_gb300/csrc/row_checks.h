@@ -15,9 +15,9 @@
 
 namespace cb {
 
-// Blocks of `block` tokens that hold `len` tokens; not positive for len <= 0.
+// Blocks of `block` tokens that hold `len` tokens; 0 for len <= 0.
 CB_HOST_DEVICE constexpr int32_t blocks_of(int32_t len, int32_t block) {
-  return len / block + (len % block > 0 ? 1 : 0);
+  return len > 0 ? (int32_t)(((uint32_t)len + (uint32_t)block - 1u) / (uint32_t)block) : 0;
 }
 
 // A row of at least one token whose table of max_blocks entries holds it.
