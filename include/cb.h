@@ -522,7 +522,8 @@ cb_status cb_attention_read_errors(void* workspace, size_t workspace_bytes,
  * cb_trim_tables shortens rows to keep_lens[r] tokens (negative, or equal to
  * cached_lens[r]: the row stays; 0: its request ended): the blocks past
  * ceil(keep / block_size) go to the ring's tail, in row order then table
- * order, their table entries become -1, cached_lens[r] = keep.  A row with
+ * order, their table entries become -1, cached_lens[r] = keep.  The cache
+ * itself is not touched (see cb_kv_append_q8 for scales).  A row with
  * keep_lens[r] > cached_lens[r], or with more blocks than its table, stays
  * (CB_DEVERR_SEQ_RANGE); from the first row whose blocks would overfill the
  * ring on, every row that gives blocks stays (CB_DEVERR_NO_BLOCKS).  An id
@@ -659,6 +660,10 @@ cb_status cb_rope(const cb_rope_args* args, cb_stream_t stream);
  *     (CB_DEVERR_SLOT_ORDER); with runs of one block that are not
  *     neighbours the block's contents are undefined (CB_VALIDATE=1 finds
  *     those).  A slot outside the pool is skipped (CB_DEVERR_SLOT_RANGE).
+ *   - a scale only grows until its block starts afresh.  Tokens that are
+ *     taken back (cb_trim_tables gives back pages, nothing else) may have
+ *     raised the scale of a block that stays; the codes before them then keep
+ *     the larger step.
  *   - rope (optional): k is rotated in float32 before it is quantised, and
  *     q [num_tokens][Hq][D] (optional) is rotated into q_out.  rot_dim is
  *     then a multiple of 16.
@@ -693,7 +698,13 @@ cb_status cb_kv_append_q8(const cb_append_q8_args* args, cb_stream_t stream);
 /* cb_paged_attention over an 8-bit cache: the same rows, masks, workspace,
  * padding and error bits; q and out are of args->dtype, args->k_cache and
  * v_cache hold codes.  Any number of query heads per KV head.  after_append
- * refers to this step's cb_kv_append_q8. */
+ * refers to this step's cb_kv_append_q8.
+ * Precision: products and sums are float32.  With bfloat16 queries the
+ * weights of the values are rounded to halves (2^-11 of a weight at most;
+ * the sum that divides them is not rounded).  With float32 queries both
+ * queries and weights are held in two halves: 22 bits, and weights to
+ * 2^-24.5 of the row's largest (a result's error is about 1e-6 of its norm;
+ * there is no mode with more bits). */
 cb_status cb_paged_attention_q8(const cb_attention_args* args, const uint8_t* k_scales,
                                 const uint8_t* v_scales, int64_t scale_stride,
                                 cb_stream_t stream);

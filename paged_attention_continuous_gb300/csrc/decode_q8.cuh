@@ -30,7 +30,8 @@
 //   * Queries are scaled by a power of two to the halves' range for each
 //     head, so that bfloat16 queries are halves exactly (elements under
 //     2^-29 of the head's largest lose bits); float32 queries are split into
-//     two halves (22 bits), and their weights too.  With those, score
+//     two halves (22 bits), and their weights too (and to 2^-24, the least
+//     half, where the largest is 2^-0.5 at least).  With those, score
 //     exponents are rounded at their size next to the reference: scale *
 //     log2(e) is a pair of floats, the reference a whole number.
 //   * Scales never touch the codes.  With x = score * log2(e), the weight

@@ -23,8 +23,9 @@
 // Every new element is read once and every code written once; HBM bounds
 // large calls and the launch with two dependent loads (slots, then the
 // block's scale) small ones.  Measured on the GPU alone, bf16, 8 heads of
-// 128: 6.9k tokens of 16 chunks 10.6 us (4.0 TB/s), 96 tokens with 32 heads
-// of q turned 4.5 us, the 6.9k with 32 heads of q turned 33.5 us (4.6 TB/s).
+// 128: 6.9k tokens of 16 chunks 10.9 us (3.9 TB/s), 96 tokens with 32 heads
+// of q turned 4.5 us, the 6.9k with 32 heads of q turned 33.8 us (4.6 TB/s);
+// float32 17.7 us and 57.2 (5.2 TB/s).
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -383,9 +384,9 @@ extern "C" cb_status cb_kv_append_q8(const cb_append_q8_args* args, cb_stream_t 
   p.error_word = a.error_word;
   // Decode steps bring runs of one token and want a warp for each, chunks
   // runs of 16 whose other tokens leave warps idle; the call cannot tell them
-  // apart.  96 decodes take 4.4 / 5.9 / 15.4 us with 1 / 4 / 16 tokens to a CTA,
-  // 1024 16.1 / 14.8 / 21.1, a chunk of 1000 tokens 5.8 / 5.0 / 3.8, 2048
-  // decodes 32.1 / 28.3 / 27.8, chunks of 2000 in all 8.2 / 6.1 / 4.4.
+  // apart.  96 decodes take 4.5 / 6.0 / 16.4 us with 1 / 4 / 16 tokens to a CTA,
+  // 600 10.0 / 9.7 / 16.6, 1024 16.2 / 14.8 / 21.2, 2048 32.0 / 28.2 / 27.9; a
+  // chunk of 600 tokens 4.6 / 4.1 / 3.1, four of 500 8.1 / 6.1 / 4.5.
   p.tokens_per_cta = a.num_tokens <= 256 ? 1 : a.num_tokens <= 1024 ? 4 : kMaxTokens;
   const bool f32 = a.dtype == CB_DTYPE_F32;
   const cudaStream_t s = (cudaStream_t)stream;

@@ -34,7 +34,7 @@
 //     float32: the unit takes 4 cycles a warp for them and 8 for a pair of
 //     halves or bfloat16s, so the packed forms only lose bits.
 //   * float32 queries: Q and the weights are split into two halves each (22
-//     bits), one query tile per CTA (the second tile's place holds the low
+//     bits; a weight also to 2^-24, the least half), one query tile per CTA (the second tile's place holds the low
 //     halves).  Score exponents are rounded once: scale * log2(e) is a pair
 //     of floats, the reference a whole number near the largest exponent.  The
 //     tensor core drops bits wherever it adds to a large accumulator, so each
@@ -48,20 +48,24 @@
 //     those two (with a window a row may see neither) it looks at the codes
 //     again, which only calls with several such codes in one dim pay for.
 //
-//   * Few rows with many keys would leave most SMs idle: when the CTAs fill
-//     less than half of them, each one's KV tiles are split over as many CTAs
-//     as there are SMs for (at least four tiles each), which leave float32
-//     parts that a second kernel joins (64 tokens of 64 heads behind 16k: 61
-//     us, 265 without; 16 tokens of 32 heads behind 100k: 169 and 1344; 64 of
-//     32 behind 2k: 26 and 44; 64 behind 900, under eight tiles: not split).
+//   * Few rows with many keys would leave most SMs idle: when the CTAs, counted
+//     by their bound (one pair more for each row than its tokens fill: the host
+//     does not know the rows), fill less than half of them, each one's KV tiles
+//     are split over SMs / bound CTAs (at least four tiles each), which leave
+//     float32 parts that a second kernel joins.  One row of 16 tokens counts
+//     two pairs where one works, so its splits fill 72 of 152 SMs (64 tokens of
+//     64 heads behind 16k: 63 us, 265 without; 16 tokens of 32 heads behind
+//     100k: 170 and 1344; 64 of 32 behind 2k: 26 and 44; 64 behind 900, under
+//     eight tiles: not split).
 //
 // What bounds it: the chain of a KV tile, 2.0 us for 128 keys and both query
 // tiles.  Its products are 1.4 us at the measured matrix rate, its 32k exponentials
 // 0.55 us of the four exponential units each, and shared memory moves codes,
 // halves and operands for 1.3 us; the rest is the turns that the two query
 // tiles' softmax take with them.  512 tokens of 64 heads behind 16k (128
-// CTAs of 152 SMs): 277 us, 1.0 PFLOP/s, 54% of the measured bfloat16 rate;
-// a CTA costs 7 us beside its tiles.
+// CTAs of 152 SMs): 279 us, 1.0 PFLOP/s, 54% of the measured bfloat16 rate
+// (with the 16-bit cache, which is read and not expanded, the 16-bit kernel
+// takes 237 us where this one takes 273); a CTA costs 7 us beside its tiles.
 //
 // Tensor memory: S0 | S1 | O0 | O1 at columns 0, 128, 256, 384; P_t is
 // written over S_t as half pairs and read from there as the A operand.

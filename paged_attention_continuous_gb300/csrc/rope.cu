@@ -13,8 +13,8 @@
 // Measured on the GPU alone, bf16, 128 dims: 8192 tokens of 64 + 8 heads 47.2
 // us interleaved with half of the dims rotated (6.4 TB/s, 96% of the measured
 // copy rate; every element, rotated or not, is read and written), 47.8 in the
-// half layout and 48.8 interleaved with all rotated; 64 tokens of 32 + 8
-// heads 2.8 us.
+// half layout and 49.1 interleaved with all rotated; 64 tokens of 32 + 8
+// heads 2.5 us; float32, 4096 tokens of 64 + 8 heads 47.5 us in either layout.
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -50,8 +50,8 @@ cb_status launch(Params& p, cudaStream_t stream) {
   Rows& r = p.rows;
   cut_rows(&r, N, kHalf);
   // tokens per CTA: one while the tokens fit the SMs' resident CTAs once
-  // (latency: 64 tokens 2.5 us, 3.8 with four; 608 3.3 and 3.9), then four, so
-  // that a CTA's loads cover its set-up (2048 tokens 10.6 us with one, 9.5)
+  // (latency: 64 tokens 2.5 us, 3.8 with four; 608 3.3 and 4.0), then four, so
+  // that a CTA's loads cover its set-up (2048 tokens 10.3 us with one, 9.2)
   p.tokens_per_cta = p.num_tokens <= 8 * sm_count_current_device() ? 1 : 4;
   const uint64_t items = (uint64_t)p.tokens_per_cta * r.heads * r.units;
   if (items * (uint64_t)(r.units > r.heads ? r.units : r.heads) >= 0x100000000ull)

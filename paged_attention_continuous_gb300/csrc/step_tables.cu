@@ -17,7 +17,7 @@
 // the reads of the state from its writes, and the CTAs share the tokens and
 // pages.  No atomics and no scratch: the order of the blocks is the rows'.
 // Measured on the GPU alone, a step and the trim that takes it back: 64 rows
-// of one token 9.9 us, 1000 rows of 37k tokens in all 15.2 us (the bytes of
+// of one token 9.5 us, 1000 rows of 37k tokens in all 14.9 us (the bytes of
 // the latter take 0.06 us).
 #include <cuda_runtime.h>
 
