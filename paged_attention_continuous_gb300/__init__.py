@@ -435,6 +435,15 @@ def _stream_ptr(stream) -> int:
     return int(stream.cuda_stream)
 
 
+def _on(stream):
+    """Makes ``stream`` current (None: nothing changes); any object with a
+    ``cuda_stream`` handle."""
+    cuda = _torch().cuda
+    if stream is not None and not isinstance(stream, cuda.Stream):
+        stream = cuda.ExternalStream(int(stream.cuda_stream))
+    return cuda.stream(stream)
+
+
 def _new_like(t, stream):
     """An uninitialised contiguous tensor like t, to be written on ``stream``
     (None: the current one).  It belongs to that stream, as if the caller had
@@ -443,7 +452,7 @@ def _new_like(t, stream):
     torch = _torch()
     if stream is None:
         return torch.empty_like(t, memory_format=torch.contiguous_format)
-    with torch.cuda.stream(stream):
+    with _on(stream):
         return torch.empty_like(t, memory_format=torch.contiguous_format)
 
 
@@ -538,7 +547,7 @@ class Workspace:
         torch = _torch()
         self.nbytes = workspace_size(max_reqs, num_q_heads, num_kv_heads, head_dim)
         self.max_reqs = max_reqs
-        with torch.cuda.stream(stream):      # (None: the current one)
+        with _on(stream):
             self.buf = torch.empty(self.nbytes + 256, dtype=torch.uint8, device=device)
         off = (-self.buf.data_ptr()) % 256
         self.ptr = self.buf.data_ptr() + off
@@ -790,7 +799,7 @@ def rope(q, k, positions, plan: RopePlan, *, q_out=None, k_out=None, inverse: bo
             and _torch().is_grad_enabled():
         if q_out is not None or k_out is not None:
             raise ValueError("rope: outputs cannot be given where a gradient is recorded")
-        with _torch().cuda.stream(stream):      # (None: the current one); the backward runs there too
+        with _on(stream):      # the backward runs there too
             return _rope_function().apply(q, k, positions, plan, inverse)
     first = q if q is not None else k
     if first is None:
@@ -899,7 +908,8 @@ def paged_attention_q8(q, k_cache, v_cache, k_scales, v_scales, cu_seqlens_q, se
                        scale: float, workspace: Workspace, out=None, stream=None,
                        sliding_window: int = 0, after_append: bool = False):
     """cb_paged_attention_q8: ``paged_attention`` over an 8-bit cache (see
-    ``kv_append_q8``); q and out are bf16 or f32."""
+    ``kv_append_q8``); q and out are bf16 or f32 (include/cb.h says what is
+    rounded).  Not differentiable."""
     dev, st = _launch_on(q, stream)
     (nb, hkv, bs, d), ss, kc, vc, ks, vs = _q8(dev, k_cache, v_cache, k_scales, v_scales)
     if out is None:

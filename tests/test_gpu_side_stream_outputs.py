@@ -18,7 +18,7 @@ def owner(t):
     return found[0]
 
 
-@pytest.mark.parametrize("side", [True, False])
+@pytest.mark.parametrize("side", [True, "handle", False])
 def test_missing_outputs_belong_to_the_launch_stream(side):
     T, hq, hkv, D, nb = 4, 8, 2, 128, 6
     dev = lambda x: torch.tensor(x, dtype=torch.int32).cuda()  # noqa: E731
@@ -36,6 +36,9 @@ def test_missing_outputs_belong_to_the_launch_stream(side):
     del spare
     torch.cuda.synchronize()
     s = torch.cuda.Stream()
+    keep, want = s, s.cuda_stream
+    if side == "handle":           # any object with a stream's handle
+        s = type("Handle", (), {"cuda_stream": s.cuda_stream})()
     if side:
         ws = cb.Workspace(1, hq, hkv, D, stream=s)
         rq, rk = cb.rope(q, k, pos, plan, stream=s)
@@ -43,7 +46,6 @@ def test_missing_outputs_belong_to_the_launch_stream(side):
         o8 = cb.paged_attention_q8(aq, *codes, *scales, *meta, workspace=ws, stream=s, **kw)
         cb.kv_append(rk, v, slots, *cache, stream=s)
         o16 = cb.paged_attention(rq, *cache, *meta, workspace=ws, stream=s, **kw)
-        want = s.cuda_stream
     else:
         ws = cb.Workspace(1, hq, hkv, D)
         rq, rk = cb.rope(q, k, pos, plan)
@@ -53,6 +55,7 @@ def test_missing_outputs_belong_to_the_launch_stream(side):
         o16 = cb.paged_attention(rq, *cache, *meta, workspace=ws, **kw)
         want = torch.cuda.current_stream().cuda_stream
     torch.cuda.synchronize()
+    del keep
     assert [owner(t) for t in (ws.buf, rq, rk, aq, o8, o16)] == [want] * 6
     # the last row's chunk of four tokens, by the plain formula
     turned = rq.float().view(T, hkv, hq // hkv, D), rk.float()
