@@ -472,7 +472,9 @@ typedef struct cb_attention_args {
 /* Workspace bytes for calls with up to num_reqs rows and these head sizes
  * (0 on bad args).  One workspace serves any later call with at most that
  * many rows and the same head sizes; the regions that carry state between
- * calls sit at fixed offsets.  num_kv_heads <= 64. */
+ * calls sit at fixed offsets.  Calls that share one run one after the other,
+ * replayed graphs of them too: two at once would overwrite each other's
+ * partials and tickets.  num_kv_heads <= 64. */
 size_t cb_attention_workspace_size(int32_t num_reqs, int32_t num_q_heads,
                                    int32_t num_kv_heads, int32_t head_dim);
 

@@ -540,7 +540,8 @@ def workspace_size(num_reqs: int, num_q_heads: int, num_kv_heads: int, head_dim:
 
 
 class Workspace:
-    """Device scratch for cb_paged_attention (zeroed once on creation)."""
+    """Device scratch for cb_paged_attention and cb_paged_attention_q8 (zeroed
+    once on creation).  Calls that share one run one after the other."""
 
     def __init__(self, max_reqs: int, num_q_heads: int, num_kv_heads: int, head_dim: int,
                  device="cuda", stream=None):
