@@ -12,8 +12,9 @@ scales, [16][D / 32] bytes.  A scale byte b stands for the half with the bits
 b << 7 (five bits of exponent, three of mantissa); b is at most 0xb7 (240), or
 0xff where the group holds an element that is not finite.  A group is 32
 neighbouring dims of a token and head, and an element's value is (n - 8) times
-its group's scale, n its code.  The codes of four neighbouring dims make a 16-bit
-word, ascending from its low four bits, which is stored rotated left by two bits.
+its group's scale, n its code.  The codes of dims 8 j to 8 j + 7 make two 16-bit
+words, the even dims and the odd ones, ascending from the low four bits; each
+is stored rotated left by two bits.
 """
 import math
 import random
@@ -212,17 +213,18 @@ def _quantised(x, dtype=torch.float64):
 
 def _packed(n):
     """Codes [..., D] as bytes [..., D / 2]."""
-    u = n.unflatten(-1, (-1, 4))
-    u = u[..., 0] | u[..., 1] << 4 | u[..., 2] << 8 | u[..., 3] << 12
+    u = n.unflatten(-1, (-1, 4, 2))
+    u = u[..., 0, :] | u[..., 1, :] << 4 | u[..., 2, :] << 8 | u[..., 3, :] << 12     # [..., D / 8, even or odd]
     u = u << 2 & 0xFFFF | u >> 14
-    return torch.where(u >= 1 << 15, u - (1 << 16), u).to(torch.int16).view(torch.uint8)
+    return torch.where(u >= 1 << 15, u - (1 << 16), u).to(torch.int16).flatten(-2).view(torch.uint8)
 
 
 def _unpacked(b):
     """Codes [..., D] of bytes [..., D / 2]."""
     u = b.contiguous().view(torch.int16).to(torch.int32) & 0xFFFF
-    shift = torch.tensor([0, 4, 8, 12], dtype=torch.int32, device="cuda")
-    return ((u >> 2 | u << 14)[..., None] >> shift & 15).flatten(-2)
+    u = (u >> 2 | u << 14).unflatten(-1, (-1, 1, 2))
+    shift = torch.tensor([0, 4, 8, 12], dtype=torch.int32, device="cuda")[:, None]
+    return (u >> shift & 15).flatten(-3)
 
 
 def _scale_of(b):
@@ -465,8 +467,8 @@ def _exact_values(cache):
     e, m = torch.floor(b / 8), b % 8
     scale = torch.where(e > 0, (1 + m / 8) * torch.exp2(e - 15), m * 2.0 ** -17)
     scale[248:] = math.nan
-    x = cache[:, :, :BS].to(torch.int64).unflatten(-1, (-1, 2))
-    x = codes[x[..., 0] + 256 * x[..., 1]].flatten(-2)
+    x = cache[:, :, :BS].to(torch.int64).unflatten(-1, (-1, 2, 2))          # [.., words of 8 dims, even or odd, bytes]
+    x = codes[x[..., 0] + 256 * x[..., 1]].transpose(-1, -2).flatten(-3)
     s = scale[cache[:, :, BS].long()].unflatten(-1, (BS, -1))
     return x * s.repeat_interleave(GROUP, -1)
 
