@@ -724,10 +724,10 @@ cb_status cb_paged_attention_q8(const cb_attention_args* args, const uint8_t* k_
  * half and a bfloat16 exactly.  Scales belong to tokens: an append never
  * touches what other tokens hold, and a token and head take 17 / 32 of the
  * 8-bit cache's bytes, 17 / 64 of the 16-bit one's.
- * Places of codes: the codes of dims 4 u .. 4 u + 3 are bytes 2 u and 2 u + 1 of
- * a row, a 16-bit word (low byte first) in which they ascend from its low four
- * bits and which is then rotated left by two bits (what the attention's
- * expansion wants).
+ * Places of codes: the codes of dims 8 j .. 8 j + 7 are bytes 4 j .. 4 j + 3 of a
+ * row, two 16-bit words (low byte first), the even dims and then the odd ones,
+ * in which they ascend from the low four bits; each word is then rotated left by
+ * two bits (what the attention's expansion wants).
  *
  * cb_kv_append_q4 writes a step's new K/V.  A group's scale is the least s
  * with |x| <= 7.5 s for all of it (240 if there is none), and a code is 8 +

@@ -30,8 +30,9 @@
 //     are loaded as 16-byte vectors: the contraction over the dims has no
 //     order, so lane qd of a row takes its quarter qd, a group (or half of
 //     one), and Q^T is loaded in the same order.  V codes come through
-//     transposing loads of 16 bits, four dims of two tokens to a lane; the
-//     output's rows are the dims in that order.
+//     transposing loads of 16 bits, four codes (every other of eight dims) of two
+//     tokens to a lane; two lanes exchange their even and odd dims at an item's
+//     end.
 //   * Queries are scaled by a power of two to the halves' range for each
 //     head, so that bfloat16 queries are halves exactly (elements under
 //     2^-29 of the head's largest lose bits); float32 queries are split into
@@ -452,9 +453,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_kernel(const __grid_con
         for (int s = 0; s < 4; ++s)
 #pragma unroll
           for (int hlf = 0; hlf < 2; ++hlf) {
-            // (pairs are four dims apart, see q4::halves8)
-            const int e = 8 * (s >> 1) + 2 * (s & 1) + hlf;
-            const float a = live ? x[j][e] * up : 0.f, b = live ? x[j][e + 4] * up : 0.f;
+            const int e = 4 * s + 2 * hlf;
+            const float a = live ? x[j][e] * up : 0.f, b = live ? x[j][e + 1] * up : 0.f;
             const __half2 h = __floats2half2_rn(a, b);
             qb[0][nt][j * 4 + s][hlf] = as_u32(h);
             if constexpr (kP == 2) {
@@ -601,9 +601,10 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_kernel(const __grid_con
         l_run[nt][1] = sum[1];
       }
       // ---- O^T += V^T P^T ----------------------------------------------------------
-      // Lane (grp, qd) holds the codes of dims 4 grp .. 4 grp + 3 of a group
-      // of 32, of tokens 2 qd and 2 qd + 1 of either half page; row grp of
-      // tile 2 c + u stands for dim 2 u of these, row grp + 8 for dim 2 u + 1.
+      // Lane (grp, qd) holds the codes of sixteen grp of a group of 32 dims (of
+      // eight of them, from 8 (grp / 2) on, the even dims or the odd ones), of
+      // tokens 2 qd and 2 qd + 1 of either half page; row grp of tile 2 c + u
+      // stands for its code 2 u, row grp + 8 for its code 2 u + 1.
       uint32_t sc[kPages][2][2];   // a token's scale bytes; masked tokens: 0
 #pragma unroll
       for (int k = 0; k < kPages; ++k)
@@ -681,8 +682,9 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_kernel(const __grid_con
     bool last = false;  // the partial before this one completed its row
     if (split && pending) last = count(ws.pend[pend_at]);
     {
-      // this lane's elements of a head: dims 32 c + 4 grp and the next three,
-      // of tiles 2 c and 2 c + 1
+      // A lane and the one whose grp is 1 less or more have the even and the odd
+      // ones of eight dims of a group: they exchange two elements, so that this
+      // lane's are dims 32 x + 4 grp and the next three.
       const int64_t base = split ? (int64_t)d.slot * Hq + d.h0 : (int64_t)d.token * Hq + d.h0;
 #pragma unroll
       for (int nt = 0; nt < kNT; ++nt)
@@ -692,22 +694,27 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_kernel(const __grid_con
 #pragma unroll
           for (int o = 4; o < 32; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
           const int h = nt * 8 + 2 * qd + c;
-          if (h < d.heads) {
-            const float inv = split ? 1.f : 1.f / l;
+          const bool in = h < d.heads, odd = grp & 1;
+          const float inv = split ? 1.f : 1.f / l;
 #pragma unroll
-            for (int x = 0; x < kGroups; ++x) {
-              const float o[4] = {acc[nt][2 * x][c] * inv, acc[nt][2 * x][c + 2] * inv,
-                                  acc[nt][2 * x + 1][c] * inv, acc[nt][2 * x + 1][c + 2] * inv};
-              const int64_t e = (base + h) * D + 32 * x + 4 * grp;
-              if (split || kP == 2)
-                *reinterpret_cast<float4*>((split ? p.part_acc : static_cast<float*>(p.out)) + e) =
-                    make_float4(o[0], o[1], o[2], o[3]);
-              else
-                *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + e) =
-                    make_uint2(float2_to_bf16x2(o[0], o[1]), float2_to_bf16x2(o[2], o[3]));
+          for (int x = 0; x < kGroups; ++x) {
+            float o[4];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const float a = acc[nt][2 * x][c + 2 * i] * inv, b = acc[nt][2 * x + 1][c + 2 * i] * inv;
+              const float mine = odd ? b : a, other = __shfl_xor_sync(0xffffffffu, odd ? a : b, 4);
+              o[2 * i] = odd ? other : mine;
+              o[2 * i + 1] = odd ? mine : other;
             }
-            if (split && grp == 0) *reinterpret_cast<float2*>(p.part_ml + (base + h) * 2) = make_float2(m_run[nt][c], l);
+            const int64_t e = (base + h) * D + 32 * x + 4 * grp;
+            if (in && (split || kP == 2))
+              *reinterpret_cast<float4*>((split ? p.part_acc : static_cast<float*>(p.out)) + e) =
+                  make_float4(o[0], o[1], o[2], o[3]);
+            else if (in)
+              *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + e) =
+                  make_uint2(float2_to_bf16x2(o[0], o[1]), float2_to_bf16x2(o[2], o[3]));
           }
+          if (in && split && grp == 0) *reinterpret_cast<float2*>(p.part_ml + (base + h) * 2) = make_float2(m_run[nt][c], l);
         }
     }
     if (last) merge(ws.pend[pend_at]);

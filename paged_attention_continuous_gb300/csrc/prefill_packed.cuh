@@ -19,9 +19,7 @@
 //     the next tile's copies at once, expand it to halves (every e4m3 number is
 //     one exactly: one conversion for two codes; a 4-bit code times its scale
 //     is one too, see q4.cuh) and store those in the swizzled layout that the
-//     matrix instructions read.  (Four dims apart are two 4-bit codes that
-//     become a pair of halves; so Q's rows, and the columns of the output,
-//     have each eight dims in that order.)  (Reading the codes
+//     matrix instructions read.  (Reading the codes
 //     from global memory into the converters' registers instead was 2.3 times
 //     slower: with 227 KB of shared memory in use the L1 holds too few
 //     outstanding loads.)
@@ -796,8 +794,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         uint32_t h[4], lo[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          // (4-bit codes: each eight dims in the order of q4::halves8)
-          const float a = x[F::kFour ? e : 2 * e] * up, b = x[F::kFour ? e + 4 : 2 * e + 1] * up;
+          const float a = x[2 * e] * up, b = x[2 * e + 1] * up;
           h[e] = halves(a, b);
           const float2 f = floats(h[e]);
           lo[e] = halves(a - f.x, b - f.y);
@@ -1002,18 +999,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
           }
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e] *= inv;
-          if constexpr (F::kFour) {
-            // each eight columns back to the order of their dims
-#pragma unroll
-            for (int b = 0; b < 32; b += 8) {
-              const float x[8] = {o[b], o[b + 1], o[b + 2], o[b + 3], o[b + 4], o[b + 5], o[b + 6], o[b + 7]};
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                o[b + e] = x[2 * e];
-                o[b + 4 + e] = x[2 * e + 1];
-              }
-            }
-          }
           if (parted) {
             // 32 dims of this split's part, in float32, row by row
             store_part(turn, c, o);

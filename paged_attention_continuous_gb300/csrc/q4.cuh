@@ -11,12 +11,13 @@
 // group that held an element that is not finite reads as NaN.
 //
 // Codes lie so that pairs of halves cost one logic operation each.  The codes
-// of four neighbouring dims are 16 bits, ascending from the low four, rotated
-// left by two.  Bits 5..2 are then the code of dim 0 and bits 9..6 that of dim
-// 1, in the middle and at the top of a half's mantissa; with the two bytes
-// exchanged the same places hold dims 2 and 3.  A 32-bit word of two such
-// sixteens (two sets of dims, or two tokens) gives pairs of halves, one from
-// each.  With exponents put above them they are the
+// of dims 8 j .. 8 j + 7 are a 32-bit word: the even dims its low 16 bits, the
+// odd ones its high 16, ascending from the low four, each sixteen then rotated
+// left by two.  Bits 5..2 of a sixteen are then its first code and bits 9..6 its
+// second, in the middle and at the top of a half's mantissa; with the two bytes
+// exchanged the same places hold its third and fourth.  So a word gives the pairs
+// of neighbouring dims, in their order, and a 32-bit word of the same sixteen of
+// two tokens gives pairs of tokens.  With exponents put above them they are the
 // halves 16 + n and 256 + n, and one fused multiply-add gives (16 + n) s - 24 s
 // or (256 + n) s - 264 s = (n - 8) s.  Both constants are halves exactly (24 s
 // has 6 bits, 264 s ten), which is why s ends at 240.
@@ -64,8 +65,8 @@ __device__ __forceinline__ float rcp_approx(float x) {
   return y;
 }
 
-// The codes of two sets of four neighbouring dims, as 16 bits each, rotated
-// left by two bits each.
+// Two sixteens (the even dims' codes and the odd ones'), rotated left by two bits
+// each.
 __device__ __forceinline__ uint32_t turn_units(uint32_t w) {
   return (w << 2 & 0xfffcfffcu) | (w >> 14 & 0x00030003u);
 }
@@ -92,11 +93,11 @@ struct Rounder {
     if (fabsf(d) > ((n & 1) ? below : half)) n += (__float_as_int(d) >> 31) | 1;
     return n;  // its low 16 bits: those of the rounded number
   }
-  __device__ __forceinline__ uint32_t four(const float* x) const {
-    return (uint32_t)(code(x[0]) + code(x[1]) * 16 + code(x[2]) * 256 + code(x[3]) * 4096 + 0x8888) & 0xffffu;
+  __device__ __forceinline__ uint32_t four(const float* x) const {  // of every other dim
+    return (uint32_t)(code(x[0]) + code(x[2]) * 16 + code(x[4]) * 256 + code(x[6]) * 4096 + 0x8888) & 0xffffu;
   }
   __device__ __forceinline__ uint32_t word(const float (&x)[8]) const {
-    return turn_units(four(x) | four(x + 4) << 16);
+    return turn_units(four(x) | four(x + 1) << 16);
   }
 };
 
@@ -127,12 +128,8 @@ struct RounderBf16 {
     const uint32_t past = __hgt2_mask(v(d & 0x7fff7fffu), v(half - (u(y) & 0x00010001u)));
     return (u(__hadd2(y, v(((d & 0x80008000u) | 0x3f803f80u) & past))) ^ 0x00080008u) & 0x000f000fu;
   }
-  __device__ __forceinline__ uint32_t four(uint32_t a, uint32_t b) const {
-    const uint32_t t = two(a) | two(b) << 8;
-    return (t | t >> 12) & 0xffffu;
-  }
   __device__ __forceinline__ uint32_t word(const uint4& x) const {
-    return turn_units(four(x.x, x.y) | four(x.z, x.w) << 16);
+    return turn_units(two(x.x) | two(x.y) << 4 | two(x.z) << 8 | two(x.w) << 12);
   }
 };
 constexpr uint32_t kZeroUnit = 0x2222u;  // four codes of 8
@@ -191,8 +188,8 @@ __device__ __forceinline__ void values8(uint32_t w, uint32_t byte, float (&x)[8]
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
-    x[i] = f.x;
-    x[4 + i] = f.y;
+    x[2 * i] = f.x;
+    x[2 * i + 1] = f.y;
   }
 }
 

@@ -23,10 +23,12 @@ def pack(n):
     """Codes [..., D] (1 to 15) as bytes [..., D / 2]."""
     n = np.asarray(n, dtype=np.int64)
     out = np.zeros(n.shape[:-1] + (n.shape[-1] // 2,), np.uint8)
-    for u in range(n.shape[-1] // 4):
-        w = sum(n[..., 4 * u + i] << (4 * i) for i in range(4))
-        w = ((w << 2) | (w >> 14)) & 0xFFFF
-        out[..., 2 * u], out[..., 2 * u + 1] = w & 0xFF, w >> 8
+    for j in range(n.shape[-1] // 8):
+        for odd in (0, 1):
+            w = sum(n[..., 8 * j + 2 * i + odd] << (4 * i) for i in range(4))
+            w = ((w << 2) | (w >> 14)) & 0xFFFF
+            out[..., 4 * j + 2 * odd] = w & 0xFF
+            out[..., 4 * j + 2 * odd + 1] = w >> 8
     return out
 
 
@@ -34,11 +36,12 @@ def unpack(b):
     """Codes [..., D] of bytes [..., D / 2]."""
     b = np.asarray(b, dtype=np.int64)
     n = np.zeros(b.shape[:-1] + (2 * b.shape[-1],), np.int64)
-    for u in range(b.shape[-1] // 2):
-        w = b[..., 2 * u] | b[..., 2 * u + 1] << 8
-        w = ((w >> 2) | (w << 14)) & 0xFFFF
-        for i in range(4):
-            n[..., 4 * u + i] = (w >> (4 * i)) & 15
+    for j in range(b.shape[-1] // 4):
+        for odd in (0, 1):
+            w = b[..., 4 * j + 2 * odd] | b[..., 4 * j + 2 * odd + 1] << 8
+            w = ((w >> 2) | (w << 14)) & 0xFFFF
+            for i in range(4):
+                n[..., 8 * j + 2 * i + odd] = (w >> (4 * i)) & 15
     return n
 
 

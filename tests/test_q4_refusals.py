@@ -30,7 +30,7 @@ def test_packing_goes_there_and_back():
     n = np.random.default_rng(0).integers(1, 16, (5, 3, 128))
     assert (ref.unpack(ref.pack(n)) == n).all()
     one = np.full(8, 8)
-    one[5] = 15                           # the second code of the second word: bits 9..6
+    one[3] = 15                           # dim 3: second code of the odd word, bits 9..6
     w = ref.pack(one).view(np.uint16)
     assert (w[1] >> 6) & 15 == 15 and (w[0] >> 6) & 15 == 8
 
