@@ -785,7 +785,8 @@ cb_status cb_kv_read_q4(const cb_read_q4_args* args, cb_stream_t stream);
 
 /* cb_paged_attention over a 4-bit cache: the same rows, masks, workspace,
  * padding and error bits; q and out are of args->dtype, args->k_cache and
- * v_cache are 4-bit caches.  Any number of query heads per KV head.
+ * v_cache are 4-bit caches.  Any number of query heads per KV head.  A page
+ * whose block lies outside the pool (CB_DEVERR_BLOCK_RANGE) reads as zeros.
  * after_append refers to this step's cb_kv_append_q4.  Precision is
  * cb_paged_attention_q8's; with float32 queries sums are kept so that a
  * result's error is about that of a plain float32 form (2 to 9e-7 of its norm

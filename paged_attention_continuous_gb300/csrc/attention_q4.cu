@@ -100,16 +100,17 @@ __global__ void __launch_bounds__(256) rows_kernel(const RowsParams p) {
   };
   for (int pg = k_lo / kPage; pg <= pos / kPage; ++pg) {
     const int blk = p.block_tables[(int64_t)r * p.max_blocks_per_seq + pg];
-    if (blk < 0 || blk >= p.num_blocks) {
-      if (lane == 0) set_error(p.error_word, CB_DEVERR_BLOCK_RANGE);
-      continue;
-    }
-    const int64_t page = ((int64_t)blk * Hkv + g) * page_bytes(D);
+    // (a page that cannot be read counts as zeros, as in the other kernels)
+    const bool there = blk >= 0 && blk < p.num_blocks;
+    if (!there && lane == 0) set_error(p.error_word, CB_DEVERR_BLOCK_RANGE);
+    const int64_t page = there ? ((int64_t)blk * Hkv + g) * page_bytes(D) : 0;
     const int i1 = min(kPage, pos + 1 - pg * kPage);
     for (int i = max(0, k_lo - pg * kPage); i < i1; ++i) {
-      float k[2 * kPairs], v[2 * kPairs];
-      values(p.k_cache + page, i, k);
-      values(p.v_cache + page, i, v);
+      float k[2 * kPairs] = {}, v[2 * kPairs] = {};
+      if (there) {
+        values(p.k_cache + page, i, k);
+        values(p.v_cache + page, i, v);
+      }
       float dot = 0.f;
 #pragma unroll
       for (int e = 0; e < 2 * kPairs; ++e) dot = fmaf(qf[e], k[e], dot);
