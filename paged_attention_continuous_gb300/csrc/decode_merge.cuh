@@ -10,11 +10,21 @@
 namespace cb {
 namespace decode {
 
+// Of four elements of every other one of eight dims (the odd ones, or those from
+// the first on, whose others the lane `away` bits aside has): the four in the
+// same places of the eight in order, which are its last or first ones.
+__device__ __forceinline__ float4 exchange_odd(float4 v, bool odd, int away) {
+  const float a = __shfl_xor_sync(0xffffffffu, odd ? v.x : v.z, away);
+  const float b = __shfl_xor_sync(0xffffffffu, odd ? v.y : v.w, away);
+  return odd ? make_float4(a, v.z, b, v.w) : make_float4(v.x, a, v.y, b);
+}
+
 // Merge the n >= 2 split partials of one item group (row, heads h0 .. h0 +
 // heads), whose slots start at s0, into the rows of query token q0: per head
 // o = sum_s 2^(m_s - M) acc_s / sum_s 2^(m_s - M) l_s, in split order.
-// kH heads at once, kB splits in flight.
-template <typename T, int D, int kH, int kB>
+// kH heads at once, kB splits in flight.  kOdd: a part's places 8 i .. 8 i + 3 hold
+// the even dims of its eight, the next four the odd ones.
+template <typename T, int D, int kH, int kB, bool kOdd = false>
 __device__ __forceinline__ void merge_splits(const float* part_ml, const float* part_acc, void* out, int Hq,
                                              int h0, int heads, int s0, int n, int q0) {
   const int lane = threadIdx.x & 31;
@@ -80,6 +90,7 @@ __device__ __forceinline__ void merge_splits(const float* part_ml, const float* 
     }
 #pragma unroll
     for (int h = 0; h < kH; ++h) {
+      if constexpr (kOdd) o[h] = exchange_odd(o[h], lane & 1, 1);
       if (hb + h < heads && lane < kV) {
         const float inv = 1.f / Ls[h];
         T* row = static_cast<T*>(out) + ((int64_t)q0 * Hq + h0 + hb + h) * D + 4 * lane;

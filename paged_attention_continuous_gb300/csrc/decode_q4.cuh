@@ -31,8 +31,8 @@
 //     order, so lane qd of a row takes its quarter qd, a group (or half of
 //     one), and Q^T is loaded in the same order.  V codes come through
 //     transposing loads of 16 bits, four codes (every other of eight dims) of two
-//     tokens to a lane; two lanes exchange their even and odd dims at an item's
-//     end.
+//     tokens to a lane; two lanes exchange their even and odd dims when a row is
+//     written.
 //   * Queries are scaled by a power of two to the halves' range for each
 //     head, so that bfloat16 queries are halves exactly (elements under
 //     2^-29 of the head's largest lose bits); float32 queries are split into
@@ -383,8 +383,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_kernel(const __grid_con
   // stores are long complete and the release rarely waits.
   auto count = [&](const ItemDesc& d) { return count_split(p.done + (int64_t)d.r * units + d.u, d.nsplit, lane); };
   auto merge = [&](const ItemDesc& d) {
-    merge_splits<T, D, 4, 4>(p.part_ml, p.part_acc, p.out, Hq, d.h0, d.heads, plan_a[d.r] + plan_b[d.r], d.nsplit,
-                             d.token);
+    merge_splits<T, D, 4, 4, true>(p.part_ml, p.part_acc, p.out, Hq, d.h0, d.heads, plan_a[d.r] + plan_b[d.r],
+                                   d.nsplit, d.token);
   };
   bool pending = false;     // ws.pend[pend_at]: the item of the partial not counted yet
   int pend_at = 0;
@@ -682,9 +682,11 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_kernel(const __grid_con
     bool last = false;  // the partial before this one completed its row
     if (split && pending) last = count(ws.pend[pend_at]);
     {
-      // A lane and the one whose grp is 1 less or more have the even and the odd
-      // ones of eight dims of a group: they exchange two elements, so that this
-      // lane's are dims 32 x + 4 grp and the next three.
+      // this lane's elements of a head: of each group of 32 dims the even or the
+      // odd ones of eight, in tiles 2 x and 2 x + 1.  A part's lie side by side
+      // (the merge puts them in order), in places 32 x + 4 grp and the next three;
+      // in a row of the output those are the dims that it has after an exchange
+      // with the lane that has the eight's others.
       const int64_t base = split ? (int64_t)d.slot * Hq + d.h0 : (int64_t)d.token * Hq + d.h0;
 #pragma unroll
       for (int nt = 0; nt < kNT; ++nt)
@@ -694,27 +696,33 @@ __global__ void __launch_bounds__(kWarps * 32, 1) decode_kernel(const __grid_con
 #pragma unroll
           for (int o = 4; o < 32; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
           const int h = nt * 8 + 2 * qd + c;
-          const bool in = h < d.heads, odd = grp & 1;
-          const float inv = split ? 1.f : 1.f / l;
+          if (!split) {
 #pragma unroll
-          for (int x = 0; x < kGroups; ++x) {
-            float o[4];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const float a = acc[nt][2 * x][c + 2 * i] * inv, b = acc[nt][2 * x + 1][c + 2 * i] * inv;
-              const float mine = odd ? b : a, other = __shfl_xor_sync(0xffffffffu, odd ? a : b, 4);
-              o[2 * i] = odd ? other : mine;
-              o[2 * i + 1] = odd ? mine : other;
+            for (int x = 0; x < kGroups; ++x) {
+              const float4 o = exchange_odd(make_float4(acc[nt][2 * x][c], acc[nt][2 * x][c + 2], acc[nt][2 * x + 1][c],
+                                                        acc[nt][2 * x + 1][c + 2]), grp & 1, 4);
+              acc[nt][2 * x][c] = o.x;
+              acc[nt][2 * x][c + 2] = o.y;
+              acc[nt][2 * x + 1][c] = o.z;
+              acc[nt][2 * x + 1][c + 2] = o.w;
             }
-            const int64_t e = (base + h) * D + 32 * x + 4 * grp;
-            if (in && (split || kP == 2))
-              *reinterpret_cast<float4*>((split ? p.part_acc : static_cast<float*>(p.out)) + e) =
-                  make_float4(o[0], o[1], o[2], o[3]);
-            else if (in)
-              *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + e) =
-                  make_uint2(float2_to_bf16x2(o[0], o[1]), float2_to_bf16x2(o[2], o[3]));
           }
-          if (in && split && grp == 0) *reinterpret_cast<float2*>(p.part_ml + (base + h) * 2) = make_float2(m_run[nt][c], l);
+          if (h < d.heads) {
+            const float inv = split ? 1.f : 1.f / l;
+#pragma unroll
+            for (int x = 0; x < kGroups; ++x) {
+              const float o[4] = {acc[nt][2 * x][c] * inv, acc[nt][2 * x][c + 2] * inv,
+                                  acc[nt][2 * x + 1][c] * inv, acc[nt][2 * x + 1][c + 2] * inv};
+              const int64_t e = (base + h) * D + 32 * x + 4 * grp;
+              if (split || kP == 2)
+                *reinterpret_cast<float4*>((split ? p.part_acc : static_cast<float*>(p.out)) + e) =
+                    make_float4(o[0], o[1], o[2], o[3]);
+              else
+                *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + e) =
+                    make_uint2(float2_to_bf16x2(o[0], o[1]), float2_to_bf16x2(o[2], o[3]));
+            }
+            if (split && grp == 0) *reinterpret_cast<float2*>(p.part_ml + (base + h) * 2) = make_float2(m_run[nt][c], l);
+          }
         }
     }
     if (last) merge(ws.pend[pend_at]);
