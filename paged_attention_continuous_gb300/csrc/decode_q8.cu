@@ -34,9 +34,9 @@ cb_status launch(const cb_attention_args& a, const uint8_t* k_scales, const uint
   if (st != CB_OK) return st;
   Params p{};
   const int64_t rows = (int64_t)a.num_blocks * a.num_kv_heads * kPageTokens;
-  st = cached_cache_map(&p.tmap_k, a.k_cache, rows, D, 1);
+  st = cached_cache_map(&p.tmap_k, a.k_cache, rows, D, CacheMap::kCodes8);
   if (st != CB_OK) return st;
-  st = cached_cache_map(&p.tmap_v, a.v_cache, rows, D, 1);
+  st = cached_cache_map(&p.tmap_v, a.v_cache, rows, D, CacheMap::kCodes8);
   if (st != CB_OK) return st;
   p.k_scales = k_scales;
   p.v_scales = v_scales;

@@ -1085,9 +1085,9 @@ cb_status launch_kernel(const cb_attention_args& a, const uint8_t* k_scales, con
   const int64_t rows = (int64_t)a.num_blocks * a.num_kv_heads * F::kRows;
   if (rows >= ((int64_t)1 << 31) - F::kRows) return CB_ERR_UNSUPPORTED;
   Params p{};
-  st = cached_cache_map(&p.tmap_k, a.k_cache, rows, D, F::kFour ? 0 : 1);
+  st = cached_cache_map(&p.tmap_k, a.k_cache, rows, D, F::kFour ? CacheMap::kCodes4 : CacheMap::kCodes8);
   if (st != CB_OK) return st;
-  st = cached_cache_map(&p.tmap_v, a.v_cache, rows, D, F::kFour ? 0 : 1);
+  st = cached_cache_map(&p.tmap_v, a.v_cache, rows, D, F::kFour ? CacheMap::kCodes4 : CacheMap::kCodes8);
   if (st != CB_OK) return st;
   p.v_cache = static_cast<const uint8_t*>(a.v_cache);
   p.k_scales = k_scales;

@@ -30,14 +30,14 @@ EncodeTiledFn encode_fn() {
 }
 
 cb_status make_cache_map(CUtensorMap* m, const void* base, int64_t rows, int head_dim,
-                         int elem_bytes) {
+                         CacheMap kind) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return fail(CB_ERR_CUDA, "cuTensorMapEncodeTiled entry point not available");
-  const cuuint32_t row = elem_bytes == 0 ? head_dim / 2 : head_dim * elem_bytes;  // bytes
-  const int elem = elem_bytes == 2 ? 2 : 1;
+  const int elem = kind == CacheMap::kBf16 ? 2 : 1;
+  const cuuint32_t row = kind == CacheMap::kCodes4 ? head_dim / 2 : head_dim * elem;  // bytes
   cuuint64_t dims[2] = {(cuuint64_t)(row / elem), (cuuint64_t)rows};
   cuuint64_t strides[1] = {(cuuint64_t)row};
-  cuuint32_t box[2] = {elem == 2 ? 64u : row, elem_bytes == 0 ? 17u : 16u};
+  cuuint32_t box[2] = {elem == 2 ? 64u : row, kind == CacheMap::kCodes4 ? 17u : 16u};
   cuuint32_t estr[2] = {1, 1};
   const cuuint32_t inner = box[0] * elem;
   CUresult r = fn(m, elem == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 2,
@@ -52,13 +52,13 @@ cb_status make_cache_map(CUtensorMap* m, const void* base, int64_t rows, int hea
 }  // namespace
 
 cb_status cached_cache_map(CUtensorMap* m, const void* base, int64_t rows, int head_dim,
-                           int elem_bytes) {
+                           CacheMap kind) {
   if (head_dim != 64 && head_dim != 128) return fail(CB_ERR_UNSUPPORTED, "tensor map head_dim %d", head_dim);
   struct Entry {
     const void* base;
     int64_t rows;
     int head_dim;
-    int elem_bytes;
+    CacheMap kind;
     CUtensorMap map;
   };
   constexpr int kEntries = 64;
@@ -68,13 +68,13 @@ cb_status cached_cache_map(CUtensorMap* m, const void* base, int64_t rows, int h
   std::lock_guard<std::mutex> lock(mu);
   for (int i = 0; i < used; ++i)
     if (entries[i].base == base && entries[i].rows == rows && entries[i].head_dim == head_dim &&
-        entries[i].elem_bytes == elem_bytes) {
+        entries[i].kind == kind) {
       *m = entries[i].map;
       return CB_OK;
     }
-  cb_status st = make_cache_map(m, base, rows, head_dim, elem_bytes);
+  cb_status st = make_cache_map(m, base, rows, head_dim, kind);
   if (st != CB_OK) return st;
-  entries[next] = Entry{base, rows, head_dim, elem_bytes, *m};
+  entries[next] = Entry{base, rows, head_dim, kind, *m};
   next = (next + 1) % kEntries;
   if (used < kEntries) ++used;
   return CB_OK;

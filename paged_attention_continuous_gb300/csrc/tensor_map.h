@@ -10,15 +10,16 @@
 
 namespace cb {
 
-// The 2-D view [rows][head_dim] of a cache laid out as
-// [num_blocks][Hkv][16][head_dim] (rows = num_blocks * Hkv * 16); rows past
-// the end read as zeros.  elem_bytes 2 (bf16): box 16 rows x 64 dims with the
-// 128-byte swizzle; 1 (8-bit codes): box 16 rows x head_dim, swizzled over
-// the row (128 or 64 bytes); 0 (4-bit codes): rows are those of [num_blocks][Hkv][17]
-// [head_dim / 2], box 17 rows x head_dim / 2 bytes, swizzled over the row (64 or
-// 32 bytes).  head_dim is 64 or 128.  Maps depend only on
-// the arguments, so the last few are kept and reused.
+// The 2-D view of a cache as rows; rows past the end read as zeros.
+enum class CacheMap {
+  kBf16,    // [num_blocks][Hkv][16][head_dim]; box 16 rows x 64 dims, 128-byte swizzle
+  kCodes8,  // the same of bytes; box 16 rows x head_dim, swizzled over the row (128 or 64 bytes)
+  kCodes4,  // [num_blocks][Hkv][17][head_dim / 2] bytes; box 17 rows x head_dim / 2, over the row (64 or 32)
+};
+
+// head_dim is 64 or 128.  Maps depend only on the arguments, so the last few
+// are kept and reused.
 cb_status cached_cache_map(CUtensorMap* m, const void* base, int64_t rows, int head_dim,
-                           int elem_bytes = 2);
+                           CacheMap kind = CacheMap::kBf16);
 
 }  // namespace cb
