@@ -558,7 +558,7 @@ def workspace_size(num_reqs: int, num_q_heads: int, num_kv_heads: int, head_dim:
 
 
 class Workspace:
-    """Device scratch for cb_paged_attention and cb_paged_attention_q8 (zeroed
+    """Device scratch for cb_paged_attention, its _q8 and its _q4 (zeroed
     once on creation).  Calls that share one run one after the other."""
 
     def __init__(self, max_reqs: int, num_q_heads: int, num_kv_heads: int, head_dim: int,

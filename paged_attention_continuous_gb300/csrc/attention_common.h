@@ -1,5 +1,5 @@
-// Workspace layout and argument checks shared by cb_paged_attention and
-// cb_paged_attention_q8.
+// Workspace layout and argument checks shared by cb_paged_attention,
+// cb_paged_attention_q8 and cb_paged_attention_q4.
 #pragma once
 
 #include <cstddef>

@@ -18,13 +18,12 @@ constexpr size_t kSmemLimit = 226 * 1024;  // of 227 KB; the plan has static wor
 constexpr int kStages = 2, kPages = 4;
 
 // Warps of a CTA: by the registers of an item's outputs and queries, what leaves
-// none of a warp's others in memory.  Measured, 8 KV heads: 64 requests of up to
-// 8k tokens, 12 warps / 8 (of three stages of two pages): 32 bfloat16 heads of 64
-// dims (24 registers) 60.6 / 60.6 us, float32 (32) 70.8 / 83.1, 128 bfloat16 heads
-// of 64 (48) 95.4 / 105.6.  128 requests of up to 32k tokens: 64 float32 heads of
-// 128 dims (64) with 12 warps of three stages of two pages 695, 8 of those 687, 8
-// of two of four 617, of three of four 617 (10 warps: 735 and more); 128 bfloat16
-// heads of 128 (96), 8 warps: 703 with three of two, 652 with two of four.
+// none of a warp's others in memory.  Measured, 8 KV heads, 12 warps / 8: 64
+// requests of up to 8k tokens, 32 bfloat16 heads of 64 dims (24 registers) 53.5 / 60
+// us, float32 (32) 61.7 / 70, 128 bfloat16 heads of 64 (48) 71.4 / 75.5.  128
+// requests of up to 32k tokens, 64 float32 heads of 128 dims (64) 714 / 553, 128
+// bfloat16 heads of 128 (96) 801 / 592.  (Three stages are no faster, stages of two
+// pages slower.)
 template <typename T, int D, int kNT>
 struct Shape {
   static constexpr int kRegs = D * kNT / 4 + D * kNT / 8 * (int)(sizeof(T) / 2);
@@ -104,10 +103,13 @@ cb_status dispatch(const cb_attention_args& a, const decode::Scratch& s, uint32_
   if (a.num_kv_heads * parts > 64) return CB_ERR_UNSUPPORTED;  // tickets, and the plan's divisions
   if ((int64_t)a.num_blocks * a.num_kv_heads >= ((int64_t)1 << 31)) return CB_ERR_UNSUPPORTED;
   // Few pages (at most this many of all KV heads' together) are read sooner by
-  // eight warps with more registers: 8 requests of up to 512 tokens 12.0 us, 13.4
-  // with twelve, 16 of up to 2k 18.6 / 20.4, 8 of up to 8k 27.9 / 30.0; 64 of up to
-  // 4k 49.6 / 46.7.  (Not beside a prefill grid: 16 of up to 4k 35.2 / 37.7, 2 of
-  // 8k 45.9 / 32.5.)
+  // eight warps with more registers: 8 requests of up to 512 tokens 12.0 us, 13.5
+  // with twelve, 16 of up to 2k 17.3 / 18.9, 8 of up to 8k 24.2 / 27.4; 64 of up to
+  // 4k 51.7 / 49.4.  (Twelve beside a prefill grid, where long rows beside long
+  // chunks want them: 96 of up to 8k and 512 tokens behind 4k 159 / 154; with 512
+  // fresh tokens 16 of up to 4k take 38 / 40, 2 of 8k 28 / 31.)
+  // The lengths are the caller's bound: a captured step declares its table's
+  // width, and with one of 128k tokens these few take 13.5, 19.4 and 30 us.
   const int64_t pages = (int64_t)a.num_decodes * a.num_kv_heads * parts * blocks_of(a.max_seq_len, q4::kPage);
   const bool few = pages <= 32768 && after != decode::After::kPrefill;
 #define CB_DEC(T, DD, NT)                                                                          \

@@ -14,14 +14,16 @@
 //     But mostly twelve warps of 168 registers,
 //     three to a scheduler, where the 8-bit kernel has eight of 255: expanding
 //     codes is arithmetic, and eight warps waited for its results in half of
-//     the cycles (128 requests of up to 32k tokens, 64 + 8 heads of 128: 441 us;
-//     429 with twelve, 458 with sixteen and steps of two pages).  So what a warp
+//     the cycles (128 requests of up to 32k tokens, 32 + 8 heads of 128: 467 us
+//     with twelve, 489 with eight; sixteen and steps of two pages took 7% longer
+//     than twelve).  So what a warp
 //     needs once an item (the plan, the item drawn next) lies in shared memory,
 //     a window of pages' places in the cache in its lanes, and what happens
 //     between steps is looked at only when some of it is due.
 //   * Pages are copied by 16-byte asynchronous copies of all lanes, 17 of them
 //     for four pages of K and V: a page is 1088 bytes, and issuing a TMA box for
-//     each took a warp a quarter of its step (563 us so, 489 with these copies).
+//     each took a warp a quarter of its step (when these copies took its place the
+//     long decodes below went from 563 us to 489).
 //     They need no barrier: a lane waits for its own group, and nothing can
 //     keep it from landing.
 //   * Codes become halves, with their scales, by one logic operation and one
@@ -50,11 +52,13 @@
 // What bounds it: the warps' instructions (305 for a page of K and V and a
 // KV head's 8 query heads, of which K's expansion and product are 85 and V's
 // 120; 55 to 60% of the issue slots), not far from memory: 128 requests of up
-// to 32k tokens 418 us, 5.1 TB/s, 75% of the measured copy rate (without the
-// arithmetic 365: pages of 1 KB lie scattered).  64 requests of up to 4k tokens
-// 47 to 50 us: 9 until the first pages have landed, everybody's at once, the rest the
-// one wave of items and their merges; 8 of up to 512 tokens 12 us, of latency.
-// The 8-bit cache takes 631, 63 and 12 us for the same.
+// to 32k tokens (64 + 8 heads of 128) 420 us, 5.1 TB/s, 75% of the measured copy
+// rate (without the arithmetic 365: pages of 1 KB lie scattered).  64 requests of up
+// to 4k tokens (32 + 8 heads) 49 us: 9 until the first pages have landed,
+// everybody's at once, the rest the one wave of items and their merges; 8 of up to
+// 512 tokens 12 us, of latency.  The 8-bit cache takes 636, 63 and 12 us for the
+// same.  (These and the figures below: passes over three states in turn, in a
+// replayed graph; requests have 32 + 8 heads of 128 dims where nothing is said.)
 #pragma once
 
 #include <cstdint>
@@ -76,15 +80,15 @@ using namespace decode;
 // How rows are cut: the 8-bit kernel's rules, but where the pages do not go in
 // one wave, one item to a warp (and its share of the last phase) up to kFewPages
 // pages of it (measured without such waves: 64 requests of up to 4k tokens, 37
-// pages to a warp, 58.5 us, 62.6 with two; up to 8k 91 and 95; 128 of up to 8k, 148
-// pages: 161 and 152; of up to 32k 534 and 439).
+// pages to a warp, 52 us, 57 with two; up to 8k 84 and 90; with them 128 of up to 8k,
+// 148 pages: 150 and 142; of up to 32k 518 and 468).
 constexpr int kFewPages = 96;
 constexpr int kItemsEven = 2;
 // One wave of items, where a warp's share of the pages is small (beside a prefill
 // grid, whose SMs come free one by one, smaller still): 64 requests of up to 4k
-// tokens 46.7 us, 50.4 in two phases; 16 of those 25.6 (27.9 with 12 warps), 32;
-// 64 of up to 8k 79.8, 83.9; one of 32k, in two phases, 30 (34 in one); 96
-// decodes of up to 8k beside 512 prompt tokens 152, 189 in one wave.
+// tokens 49.4 us, 52.1 in two phases; 16 of those 23.7 and 30; 8 of up to 8k 24 and
+// 34; 64 of up to 8k 77 and 84; 2 of 8k beside 512 prompt tokens 31 and 51; 96 of up
+// to 8k beside 512 behind 4k 154, 192 in one wave.
 constexpr int kSinglePages = 128, kSingleBeside = 32;
 constexpr int kSingleLeast = 4;
 constexpr int kMaxSplits = 64;

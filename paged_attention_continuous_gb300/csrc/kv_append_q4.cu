@@ -17,8 +17,9 @@
 // Every new element is read once and every code written once.  What bounds it:
 // in large calls the arithmetic (float32 and turned words take more than
 // bfloat16's), in small ones the launch with one dependent access.  Measured in a
-// row of calls, 8 heads of 128: 8521 tokens 11.5 us, of which HBM needs 6.5, 32768
-// tokens 32.5 (4.8 TB/s); 96 tokens with 32 heads of q turned 2.5.
+// replayed row of calls, 8 heads of 128: 8521 tokens 10.7 us, of which HBM needs
+// 6.5, 32768 tokens 31.4 (5.4 TB/s); float32 19.4 of 11.7 and 62.6 of 44.8; 96 tokens
+// with 32 heads of q turned 2.5, 8521 of those 42 of 27 (float32 62 of 53).
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -253,8 +254,8 @@ template <typename T, int D>
 cb_status dispatch(Params& p, bool with_rope, cudaStream_t stream) {
   // Words of one group in one thread share its scale and what places them, and
   // leave fewer threads: 8 heads of 128 dims, bfloat16, one / two / four words,
-  // 512 tokens 2.6 / 2.6 / 3.3 us, 2048 4.9 / 4.5 / 4.7, 8521 15.3 / 12.9 / 11.5;
-  // float32 3.1 / 3.3 / 5.5, 6.0 / 6.2 / 9.8, 21.7 / 19.1 / 37.1.
+  // 512 tokens 2.5 / 2.5 / 3.3 us, 2048 4.6 / 4.1 / 4.3, 8521 14.6 / 11.9 / 10.7;
+  // float32 3.2 / 3.4 / 5.5, 6.1 / 6.4 / 9.8, 21.9 / 19.5 / 36.8.
   constexpr int kMany = sizeof(T) == 2 ? 4 : 2;
   if (!with_rope && (int64_t)p.num_tokens * p.num_kv_heads * (D / 8) >= 1 << 18)
     return launch<T, D, kNoRope, kMany>(p, stream);

@@ -7,7 +7,8 @@
 // head, for kTokens tokens: 4 bytes of codes and a scale byte each become 16 or
 // 32 bytes, which a warp stores as whole lines.  HBM bounds it, and in it the
 // rows written (four fifths of the traffic in bfloat16): 32768 tokens of 8 heads of 128
-// dims 28.0 us, 6.1 TB/s, 90% of the measured copy rate.  Each access waits for
+// dims 29.8 us, 5.7 TB/s, 84% of the measured copy rate (float32 67 us, 4.5 TB/s; 8521
+// tokens 8.2 and 21.2).  Each access waits for
 // its token's slot, so a thread has several tokens' on the way.
 #include <cuda_runtime.h>
 
@@ -96,7 +97,8 @@ void launch_sets(const Params& p, cudaStream_t stream) {
 
 // One token to a thread spreads few tokens over more SMs, four keep more
 // loads on the way (8 heads of 128 dims, bfloat16: 16 tokens 4.7 / 5.1 us,
-// 1536 5.1 / 5.3, 8768 10.4 / 10.2, 32768 31.6 / 28.0; eight are slower again).
+// 1536 5.1 / 5.3, 8768 10.4 / 10.2, 32768 31.6 / 28.0, in one replayed call each;
+// eight are slower again).
 template <typename T, int D>
 void launch(Params& p, cudaStream_t stream) {
   p.sets = std::max(kThreads / (p.num_kv_heads * (D / 8)), 1);

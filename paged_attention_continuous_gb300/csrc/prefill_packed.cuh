@@ -118,8 +118,12 @@ constexpr int kThreads = 512;
 constexpr int kRegsSoftmax = 192, kRegsMma = 48, kRegsConv = 80;
 static_assert(128 * (2 * kRegsSoftmax + kRegsMma + kRegsConv) <= 65536, "register split");
 constexpr uint32_t kHalf = 128 * 128;  // 128 rows of 64 halves
-// A CTA costs about 7 us beside its KV tiles, of 2 us each, so a split of the
-// keys has at least four of them.
+// A CTA costs about 7 us beside its KV tiles, of 1.6 to 1.75 us each, so a split of
+// the keys has at least four of them.  Measured with at least two / three / four / six,
+// 4-bit cache (the 8-bit one within 1 us of it): 64 tokens of 64 heads behind 900
+// keys 22.5 / 25.3 / 23.7 / 23.8 us, 64 of 32 behind 2k 22.7 / 23.7 / 24.6 / 30.8,
+// 16 of 32 behind 600 18.2 / 16.2 / 16.2 / 16.2, behind 1000 18.4 / 20.3 / 20.5 /
+// 20.6, 64 of 32 behind 4k 24.9 / 24.8 / 25.7 / 28.8.
 constexpr int kLeastTiles = 4;
 constexpr int kMaxSplits = 16;
 constexpr uint32_t kTmemCols = 512;

@@ -1,5 +1,5 @@
 // Rotary positions: the angle and the rotation of one pair, shared by the
-// cb_rope kernel and the append into the 8-bit cache.
+// cb_rope kernel and the appends into the 8-bit and the 4-bit cache.
 //
 // A pair (a, b) at position p turns by p * f.  The plan holds f as a 64-bit
 // fraction of a turn, so p * turns mod 2^64 is the angle as a fraction of a
